@@ -55,6 +55,18 @@ msa_status_t check_shape_bk128(const msa_shape_t* s) {
   return s->B_k == kBk ? MSA_OK : MSA_ERR_UNSUPPORTED;
 }
 
+msa_status_t check_paged(const msa_shape_t* s, const msa_paged_t* pg) {
+  msa_status_t st = check_shape_bk128(s);
+  if (st != MSA_OK) return st;
+  if (pg == nullptr || pg->seqlens == nullptr || pg->block_table == nullptr) return MSA_ERR_INVALID_ARG;
+  if (pg->batch < 1 || pg->max_blocks < 1 || pg->num_pages < 1 || pg->max_seqlen < 1) return MSA_ERR_INVALID_ARG;
+  if (pg->max_seqlen > (int64_t)pg->max_blocks * kBk) return MSA_ERR_INVALID_ARG;
+  // key rows are int32 coordinates; cached tokens are summed in int32
+  if (pg->num_pages > (INT32_MAX - kBk) / kBk) return MSA_ERR_UNSUPPORTED;
+  if ((int64_t)pg->batch * pg->max_blocks * kBk > (int64_t)INT32_MAX - 256) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
 }  // namespace msa
 
 namespace {
@@ -234,23 +246,11 @@ msa_status_t attn_common(const msa_shape_t* shape, const msa_varlen_t* seqs, con
   return MSA_OK;
 }
 
-// Paged decode: workspace slices and argument checks.
+// Paged decode: workspace slices.
 struct PagedLayout {
   size_t cu_q, cu_k, tile_ctr, idx_scratch, total;
   int64_t total_k;   // upper bound of the cached tokens
 };
-
-msa_status_t check_paged(const msa_shape_t* s, const msa_paged_t* pg) {
-  msa_status_t st = check_shape_bk128(s);
-  if (st != MSA_OK) return st;
-  if (pg == nullptr || pg->seqlens == nullptr || pg->block_table == nullptr) return MSA_ERR_INVALID_ARG;
-  if (pg->batch < 1 || pg->max_blocks < 1 || pg->num_pages < 1 || pg->max_seqlen < 1) return MSA_ERR_INVALID_ARG;
-  if (pg->max_seqlen > (int64_t)pg->max_blocks * kBk) return MSA_ERR_INVALID_ARG;
-  // key rows are int32 coordinates; cached tokens are summed in int32
-  if (pg->num_pages > (INT32_MAX - kBk) / kBk) return MSA_ERR_UNSUPPORTED;
-  if ((int64_t)pg->batch * pg->max_blocks * kBk > (int64_t)INT32_MAX - 256) return MSA_ERR_UNSUPPORTED;
-  return MSA_OK;
-}
 
 PagedLayout paged_layout(const msa_shape_t* s, const msa_paged_t* pg) {
   PagedLayout L{};

@@ -1,0 +1,52 @@
+// msa_cache.h — the cache of a densely attended layer: launchers of its decode
+// attention (msa_dense_decode.cu), of the attention weight a prompt's queries
+// give every key (msa_attn_weights.cu) and of the eviction by accumulated
+// weight (msa_evict.cu).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace msa {
+
+struct DevError;
+
+// DevError::where of these kernels.
+constexpr int32_t kSiteDenseDecode = 241;   // lengths, pages and waits of the dense paged decode
+constexpr int32_t kSiteAttnWeights = 251;   // key weights of a prompt's queries
+constexpr int32_t kSiteEvictSelect = 261;   // a length outside its bounds
+constexpr int32_t kSiteEvictMove = 271;     // lengths, kept indices and pages of the move
+
+// CTAs of the dense paged decode (one per SM of a B200; fewer on a smaller
+// device).  A constant, so that the workspace size needs no device.
+constexpr int kDecodeCtas = 148;
+
+struct DenseDecodeArgs {
+  const void* q;              // bf16 [batch, H, d]
+  const void* k_pages;        // bf16 [num_pages * 128, G, d]
+  const void* v_pages;
+  void* out;                  // bf16 [batch, H, d]
+  float* lse;                 // [batch, H] or null
+  float* weights;             // [batch, G, max_blocks * 128] or null
+  float decay;
+  float sm_scale;
+  int32_t batch, H, G, d;
+  const int32_t* seqlens;     // [batch]
+  const int32_t* block_table; // [batch, max_blocks]
+  int32_t max_blocks, max_seqlen;
+  int64_t num_pages;
+  DevError* err;
+  // workspace slices (dense_decode_layout)
+  int32_t* seq_start;         // [batch + 1]: first tile of each sequence; [batch]: tiles in all
+  float2* stats;              // [batch, H]: maximum and sum of each head's softmax
+  float2* part_ml;            // [CTA, 2, H]
+  float* part_o;              // [CTA, 2, H, d]
+  float* logits;              // scores of every key (with weights only)
+};
+struct DenseDecodeLayout {
+  size_t seq_start, stats, part_ml, part_o, logits, total;
+};
+DenseDecodeLayout dense_decode_layout(int32_t batch, int32_t H, int32_t d, int32_t max_seqlen, bool with_weights);
+int launch_dense_decode(const DenseDecodeArgs& a, void* stream);
+
+}  // namespace msa

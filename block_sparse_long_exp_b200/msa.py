@@ -29,6 +29,7 @@ bare pointers and cannot see a buffer's size.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -57,6 +58,7 @@ EXPORTED = [
     "msa_selected_share", "msa_index_topk_policy", "msa_gather_pages",
     "msa_prefill_workspace_size", "msa_prefill", "msa_set_prefill_overlap", "msa_index_kl_workspace_size",
     "msa_sparse_attn_backward_workspace_size",
+    "msa_dense_attn_decode_paged_workspace_size", "msa_dense_attn_decode_paged",
 ]
 
 
@@ -174,6 +176,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_index_topk_policy.restype = i32
     lib.msa_gather_pages.argtypes = [P(Varlen), vp, i32, i64, i64, vp, vp, vp, sz, vp]
     lib.msa_gather_pages.restype = i32
+    f32 = ctypes.c_float
+    lib.msa_dense_attn_decode_paged_workspace_size.argtypes = [P(Shape), P(Paged), i32]
+    lib.msa_dense_attn_decode_paged_workspace_size.restype = sz
+    lib.msa_dense_attn_decode_paged.argtypes = [P(Shape), P(Paged), vp, vp, vp, vp, vp, vp, f32, vp, sz, vp]
+    lib.msa_dense_attn_decode_paged.restype = i32
     _lib = lib
     return lib
 
@@ -975,3 +982,74 @@ def msa_set_attn_window(rows: int) -> int:
 
 def msa_version() -> str:
     return load_library().msa_version().decode()
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The device of a call's tensors made current, and its stream: yields the
+    stream's handle.  What is allocated inside belongs to that stream, so that
+    a workspace or output released after an unchecked call on a side stream is
+    not handed out while the call still runs."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            return
+        if stream.device != device:
+            raise MsaError(f"stream of {stream.device}, tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _decay(decay: float) -> float:
+    if not 0.0 <= float(decay) <= 1.0:
+        raise MsaError(f"decay: {decay}, expected a number in [0, 1]")
+    return float(decay)
+
+
+def msa_dense_attn_decode_paged_workspace_size(shape: Shape, pages: Paged, with_weights: bool = False) -> int:
+    """Workspace bytes of msa_dense_attn_decode_paged (0: rejected)."""
+    return load_library().msa_dense_attn_decode_paged_workspace_size(ctypes.byref(shape), ctypes.byref(pages),
+                                                                     1 if with_weights else 0)
+
+
+def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_pages: torch.Tensor,
+                                v_pages: torch.Tensor, out: Optional[torch.Tensor] = None,
+                                lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                                weights: Optional[torch.Tensor] = None, decay: float = 1.0,
+                                ws: Optional[torch.Tensor] = None, stream=None,
+                                check: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Dense attention of one new token per sequence over paged K / V: q bf16
+    [batch, H, d], k_pages / v_pages bf16 [num_pages * 128, G, d]; returns out
+    bf16 [batch, H, d] and lse f32 [batch, H] (None with want_lse=False).
+    weights f32 [batch, G, max_blocks * 128], if given, becomes decay * weights
+    plus each key's attention weight summed over its group's heads, in place
+    (entries past a sequence's end stay).  A length of 0 is a padded row: out 0,
+    lse -inf."""
+    lib = load_library()
+    B, rows = pages.batch, pages.num_pages * 128
+    _arg("q", q, torch.bfloat16, (B, shape.H, shape.d))
+    _arg("k_pages", k_pages, torch.bfloat16, (rows, shape.G, shape.d))
+    _arg("v_pages", v_pages, torch.bfloat16, (rows, shape.G, shape.d))
+    _arg("out", out, torch.bfloat16, (B, shape.H, shape.d), optional=True)
+    _arg("lse", lse, torch.float32, (B, shape.H), optional=True)
+    _arg("weights", weights, torch.float32, (B, shape.G, pages.max_blocks * 128), optional=True)
+    decay = _decay(decay)
+    _ws_arg(ws)
+    _require_cuda(q, k_pages, v_pages, out, lse, weights, ws, *getattr(pages, "_keep", ()))
+    with _on(q.device, stream) as handle:
+        if out is None:
+            out = torch.empty((B, shape.H, shape.d), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, shape.H), dtype=torch.float32, device=q.device)
+        if ws is None:
+            need = msa_dense_attn_decode_paged_workspace_size(shape, pages, weights is not None)
+            if need == 0:
+                raise MsaError("msa_dense_attn_decode_paged: shape or paged description rejected")
+            ws = _workspace(need, q.device)
+        rc = lib.msa_dense_attn_decode_paged(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages),
+                                             _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(weights), decay, _ptr(ws),
+                                             _nbytes(ws), handle)
+        _check(rc, "msa_dense_attn_decode_paged")
+        if check:
+            _device_check(ws, stream, "msa_dense_attn_decode_paged")
+    return out, lse

@@ -448,6 +448,44 @@ msa_status_t msa_dense_attn(const msa_shape_t* shape, const msa_varlen_t* seqs,
                             void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Dense attention of one new token per sequence over the paged K / V: the
+ * decode step of a layer that attends densely, and the decode-side
+ * counterpart of msa_dense_attn (pnsm.cn sec. 9 compares the pages' decode
+ * with dense GQA; the split over the cache's length is this library's own
+ * schedule).  For head h of group g of sequence b, over its seqlens[b] tokens
+ * (the new one included),
+ *   s_j = sm_scale <q[b, h], k_j>,  lse[b, h] = log sum_j exp(s_j),
+ *   out[b, h] = sum_j exp(s_j - lse) v_j,
+ * and, if `weights` is given, what eviction by accumulated attention goes by:
+ *   weights[b, g, j] = decay weights[b, g, j] + sum over the group's heads of
+ *                      exp(s_j - lse[b, h])                 for j < seqlens[b]
+ * (decay in [0, 1]; with 0 the old value is not read).  weights has one row of
+ * max_blocks * 128 floats per (sequence, group), by position and not by page:
+ * sequences that share a page each have their own.  Entries from seqlens[b] on
+ * are not touched.
+ * Unlike the sparse decode calls, a length of 0 is a padded row and no error:
+ * out is 0, lse -inf, weights stay.  A length below 0 or above max_seqlen is
+ * recorded as MSA_ERR_DEVICE_CHECK and treated as 0; a page outside the cache
+ * too, and its tokens are left out (nothing is read out of range).  Rows of a
+ * page past the sequence's end may hold anything.  A head whose scores are all
+ * -inf gets out 0 and lse -inf.
+ * q, k_pages, v_pages and out 16-byte aligned, else MSA_ERR_INVALID_ARG.  The
+ * parts of a sequence are joined in a fixed order: results are the same from
+ * run to run (on one device model).  Workspace: with_weights != 0 adds 4 H
+ * bytes per sequence and token of max_seqlen (the scores, in 32 bits). */
+size_t msa_dense_attn_decode_paged_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages,
+                                                  int32_t with_weights);
+
+msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_paged_t* pages,
+                                         const void* q,        /* device bf16 [batch, H, d] */
+                                         const void* k_pages,  /* device bf16 [num_pages*128, G, d] */
+                                         const void* v_pages,  /* device bf16 [num_pages*128, G, d] */
+                                         void* out,            /* device bf16 [batch, H, d] (out) */
+                                         float* lse,           /* device f32 [batch, H] (out) or NULL */
+                                         float* weights, /* device f32 [batch, G, max_blocks*128] (in / out) or NULL */
+                                         float decay, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Work split of the prefill main branch (process-wide; returns the previous
  * value).  This library's own scheduling choice: the pages' kernel runs
  * KV-outer throughout (pnsm.cn sec. 7; yololab.net "KV Outer Gather Q").
@@ -582,7 +620,8 @@ msa_status_t msa_index_topk_decode_noalloc(const msa_shape_t* shape, const msa_v
  * event pair on its launch stream; msa_profile_read(name, ...) waits for those
  * events and returns the summed device time (ms) and launch count of the
  * kernel `name` ("index_topk_prefill", "decode_scan", "decode_select",
- * "sparse_attn", "combine", "count", "plan", "scatter", "dense_attn", ...).
+ * "sparse_attn", "combine", "count", "plan", "scatter", "dense_attn",
+ * "dense_decode", ...).
  * With name == NULL it returns the number of kernels launched since the last
  * msa_profile_reset (launches are counted even while timing is disabled). */
 msa_status_t msa_profile_enable(int on);
@@ -607,6 +646,8 @@ msa_status_t msa_profile_read(const char* kernel, double* total_ms, int64_t* cou
  *   191      main-branch backward                      201  policy selection
  *   211      page gather (info0 = sequence, info1 = block)
  *   221      bounded-wait self-test              231  decode candidate merge
+ *   241      dense paged decode (a length, info0 = sequence, info1 = length; a
+ *            page, info0 = sequence, info1 = block; a wait)
  * MSA_ERR_TIMEOUT codes come from a bounded wait that ran out (about a
  * second); the call's results are then not valid, the context still is. */
 msa_status_t msa_get_device_error(void* ws, int32_t* code, int32_t* where, int32_t* info0,
