@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <vector_types.h>
+
 namespace msa {
 
 struct DevError;
@@ -48,5 +50,32 @@ struct DenseDecodeLayout {
 };
 DenseDecodeLayout dense_decode_layout(int32_t batch, int32_t H, int32_t d, int32_t max_seqlen, bool with_weights);
 int launch_dense_decode(const DenseDecodeArgs& a, void* stream);
+
+struct EvictSelectArgs {
+  const float* weights;       // [batch, G, width]
+  int64_t width;              // a multiple of 128
+  const int32_t* seqlens;
+  int32_t batch, G, per_group, max_seqlen, budget, n_sink, n_recent;
+  int32_t* kept;              // [batch, per_group ? G : 1, budget]
+  int32_t* new_lens;          // [batch]
+  uint32_t* keys;             // evict_select_keys_bytes of workspace
+  DevError* err;
+};
+// Workspace for the ranking keys (0 where they fit in shared memory).
+size_t evict_select_keys_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen);
+int launch_evict_select(const EvictSelectArgs& a, void* stream);
+
+struct EvictMoveArgs {
+  const int32_t *src_lens, *src_table, *dst_lens, *dst_table;
+  const int32_t* kept;        // [batch, per_group ? G : 1, kept_width]
+  int32_t batch, src_blocks, src_max, dst_blocks, dst_max, kept_width, per_group, G, d, d_idx;
+  int64_t num_pages;
+  void *k, *v, *k_idx;        // pages, read and written
+  const float* weights;       // [batch, G, src_blocks * 128] or null
+  float* weights_out;         // [batch, G, dst_blocks * 128] or null
+  uint32_t* flags;            // [num_pages] of workspace, zeroed before the launch
+  DevError* err;
+};
+int launch_evict_move(const EvictMoveArgs& a, void* stream);
 
 }  // namespace msa

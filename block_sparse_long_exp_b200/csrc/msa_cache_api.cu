@@ -61,4 +61,66 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
   return launch_dense_decode(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
 }
 
+size_t msa_evict_select_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages, int32_t per_group) {
+  if (check_paged(shape, pages) != MSA_OK) return 0;
+  return kWsHeader + evict_select_keys_bytes(pages->batch, per_group != 0 ? shape->G : 1, pages->max_seqlen);
+}
+
+msa_status_t msa_evict_select(const msa_shape_t* shape, const msa_paged_t* pages, const float* weights,
+                              int32_t budget, int32_t n_sink, int32_t n_recent, int32_t per_group, int32_t* kept,
+                              int32_t* new_lens, void* ws, size_t ws_bytes, void* stream) {
+  const msa_status_t st = check_paged(shape, pages);
+  if (st != MSA_OK) return st;
+  if (!weights || !kept || !new_lens || !aligned(weights, 16)) return MSA_ERR_INVALID_ARG;
+  if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget) return MSA_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, msa_evict_select_workspace_size(shape, pages, per_group))) return MSA_ERR_WORKSPACE;
+  if ((int64_t)pages->batch * shape->G * 8 > INT32_MAX) return MSA_ERR_UNSUPPORTED;      // CTAs of one launch
+  if (!clear_error(ws, stream)) return MSA_ERR_CUDA;
+  EvictSelectArgs a{};
+  a.weights = weights; a.width = (int64_t)pages->max_blocks * kBk; a.seqlens = pages->seqlens;
+  a.batch = pages->batch; a.G = shape->G; a.per_group = per_group != 0; a.max_seqlen = pages->max_seqlen;
+  a.budget = budget; a.n_sink = n_sink; a.n_recent = n_recent;
+  a.kept = kept; a.new_lens = new_lens;
+  a.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  a.err = static_cast<DevError*>(ws);
+  return launch_evict_select(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
+}
+
+size_t msa_evict_move_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages) {
+  if (check_paged(shape, pages) != MSA_OK) return 0;
+  return kWsHeader + align_up(sizeof(uint32_t) * (size_t)pages->num_pages, 256);
+}
+
+msa_status_t msa_evict_move(const msa_shape_t* shape, const msa_paged_t* pages, const msa_paged_t* new_pages,
+                            const int32_t* kept, int32_t kept_width, int32_t per_group, void* k_pages, void* v_pages,
+                            void* k_idx_pages, const float* weights, float* weights_out, void* ws, size_t ws_bytes,
+                            void* stream) {
+  msa_status_t st = check_paged(shape, pages);
+  if (st != MSA_OK) return st;
+  st = check_paged(shape, new_pages);
+  if (st != MSA_OK) return st;
+  if (new_pages->batch != pages->batch || new_pages->num_pages != pages->num_pages) return MSA_ERR_INVALID_ARG;
+  if (!kept || kept_width < 1 || !k_pages || !v_pages) return MSA_ERR_INVALID_ARG;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_idx_pages, 16)) return MSA_ERR_INVALID_ARG;
+  if ((weights == nullptr) != (weights_out == nullptr) || (weights != nullptr && weights == weights_out))
+    return MSA_ERR_INVALID_ARG;
+  // the groups share the index keys: tokens kept by group have none of their own
+  if (per_group != 0 && shape->G > 1 && k_idx_pages != nullptr) return MSA_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, msa_evict_move_workspace_size(shape, pages))) return MSA_ERR_WORKSPACE;
+  if (cudaMemsetAsync(ws, 0, kWsHeader + sizeof(uint32_t) * (size_t)pages->num_pages,
+                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MSA_ERR_CUDA;
+  EvictMoveArgs a{};
+  a.src_lens = pages->seqlens; a.src_table = pages->block_table;
+  a.dst_lens = new_pages->seqlens; a.dst_table = new_pages->block_table;
+  a.kept = kept; a.batch = pages->batch; a.src_blocks = pages->max_blocks; a.src_max = pages->max_seqlen;
+  a.dst_blocks = new_pages->max_blocks; a.dst_max = new_pages->max_seqlen; a.kept_width = kept_width;
+  a.per_group = per_group != 0; a.G = shape->G; a.d = shape->d; a.d_idx = shape->d_idx;
+  a.num_pages = pages->num_pages;
+  a.k = k_pages; a.v = v_pages; a.k_idx = k_idx_pages; a.weights = weights; a.weights_out = weights_out;
+  a.flags = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  a.err = static_cast<DevError*>(ws);
+  return launch_evict_move(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
+}
+
 }  // extern "C"

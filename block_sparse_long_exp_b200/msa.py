@@ -59,6 +59,7 @@ EXPORTED = [
     "msa_prefill_workspace_size", "msa_prefill", "msa_set_prefill_overlap", "msa_index_kl_workspace_size",
     "msa_sparse_attn_backward_workspace_size",
     "msa_dense_attn_decode_paged_workspace_size", "msa_dense_attn_decode_paged",
+    "msa_evict_select_workspace_size", "msa_evict_select", "msa_evict_move_workspace_size", "msa_evict_move",
 ]
 
 
@@ -181,6 +182,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_dense_attn_decode_paged_workspace_size.restype = sz
     lib.msa_dense_attn_decode_paged.argtypes = [P(Shape), P(Paged), vp, vp, vp, vp, vp, vp, f32, vp, sz, vp]
     lib.msa_dense_attn_decode_paged.restype = i32
+    lib.msa_evict_select_workspace_size.argtypes = [P(Shape), P(Paged), i32]
+    lib.msa_evict_select_workspace_size.restype = sz
+    lib.msa_evict_select.argtypes = [P(Shape), P(Paged), vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.msa_evict_select.restype = i32
+    lib.msa_evict_move_workspace_size.argtypes = [P(Shape), P(Paged)]
+    lib.msa_evict_move_workspace_size.restype = sz
+    lib.msa_evict_move.argtypes = [P(Shape), P(Paged), P(Paged), vp, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.msa_evict_move.restype = i32
     _lib = lib
     return lib
 
@@ -1053,3 +1062,103 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
         if check:
             _device_check(ws, stream, "msa_dense_attn_decode_paged")
     return out, lse
+
+
+def msa_evict_select_workspace_size(shape: Shape, pages: Paged, per_group: bool = False) -> int:
+    """Workspace bytes of msa_evict_select (0: rejected)."""
+    return load_library().msa_evict_select_workspace_size(ctypes.byref(shape), ctypes.byref(pages),
+                                                          1 if per_group else 0)
+
+
+def msa_evict_select(shape: Shape, pages: Paged, weights: torch.Tensor, budget: int, n_sink: int = 0,
+                     n_recent: int = 0, per_group: bool = False, kept: Optional[torch.Tensor] = None,
+                     new_lens: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None,
+                     check: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The tokens that stay when every sequence of a paged cache is cut to
+    `budget`: the first n_sink, the last n_recent and the best others by
+    accumulated weight (f32 [batch, G, max_blocks * 128]; the groups' sum, or
+    with per_group each group by its own), ties to the lower position.  Returns
+    kept int32 [batch, G if per_group else 1, budget] (ascending, -1 padded) and
+    new_lens int32 [batch]."""
+    lib = load_library()
+    B, R, budget = pages.batch, shape.G if per_group else 1, int(budget)
+    if budget < 1 or n_sink < 0 or n_recent < 0 or n_sink + n_recent > budget or budget >= 2 ** 31:
+        raise MsaError(f"msa_evict_select: budget {budget}, n_sink {n_sink}, n_recent {n_recent}: expected "
+                       "budget >= 1 and n_sink + n_recent <= budget")
+    _arg("weights", weights, torch.float32, (B, shape.G, pages.max_blocks * 128))
+    _arg("kept", kept, torch.int32, (B, R, budget), optional=True)
+    _arg("new_lens", new_lens, torch.int32, (B,), optional=True)
+    _ws_arg(ws)
+    _require_cuda(weights, kept, new_lens, ws, *getattr(pages, "_keep", ()))
+    with _on(weights.device, stream) as handle:
+        if kept is None:
+            kept = torch.empty((B, R, budget), dtype=torch.int32, device=weights.device)
+        if new_lens is None:
+            new_lens = torch.empty((B,), dtype=torch.int32, device=weights.device)
+        if ws is None:
+            need = msa_evict_select_workspace_size(shape, pages, per_group)
+            if need == 0:
+                raise MsaError("msa_evict_select: shape or paged description rejected")
+            ws = _workspace(need, weights.device)
+        rc = lib.msa_evict_select(ctypes.byref(shape), ctypes.byref(pages), _ptr(weights), budget, int(n_sink),
+                                  int(n_recent), 1 if per_group else 0, _ptr(kept), _ptr(new_lens), _ptr(ws),
+                                  _nbytes(ws), handle)
+        _check(rc, "msa_evict_select")
+        if check:
+            _device_check(ws, stream, "msa_evict_select")
+    return kept, new_lens
+
+
+def msa_evict_move_workspace_size(shape: Shape, pages: Paged) -> int:
+    """Workspace bytes of msa_evict_move (0: rejected)."""
+    return load_library().msa_evict_move_workspace_size(ctypes.byref(shape), ctypes.byref(pages))
+
+
+def msa_evict_move(shape: Shape, pages: Paged, new_pages: Paged, kept: torch.Tensor, k_pages: torch.Tensor,
+                   v_pages: torch.Tensor, k_idx_pages: Optional[torch.Tensor] = None,
+                   weights: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> Optional[torch.Tensor]:
+    """Copies the kept tokens' rows (kept int32 [batch, 1 or G, width], from
+    msa_evict_select) out of `pages` into the pages of `new_pages` (its seqlens:
+    the new lengths), in the same pool: k_pages / v_pages and, if given,
+    k_idx_pages (not with a ranking per group).  weights [batch, G, max_blocks *
+    128] of `pages` gives weights_out of `new_pages` (allocated if None): the
+    kept tokens' weights, zeros from the new length on.  Returns weights_out.
+    The old pages keep their rows; a new page that is also an old one, or named
+    twice, is reported and not written."""
+    lib = load_library()
+    B, rows, G = pages.batch, pages.num_pages * 128, shape.G
+    if new_pages.batch != B or new_pages.num_pages != pages.num_pages:
+        raise MsaError("msa_evict_move: pages and new_pages describe the same sequences and pool "
+                       f"(batch {B} and {new_pages.batch}, num_pages {pages.num_pages} and {new_pages.num_pages})")
+    _arg("kept", kept, torch.int32)
+    if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] not in (1, G) or kept.shape[2] < 1:
+        raise MsaError(f"kept: shape {tuple(kept.shape)}, expected ({B}, 1 or {G}, width)")
+    per_group = kept.shape[1] == G and G > 1
+    if per_group and k_idx_pages is not None:
+        raise MsaError("msa_evict_move: the groups share the index keys; a ranking per group has none to move")
+    if weights is None and weights_out is not None:
+        raise MsaError("msa_evict_move: weights_out without weights")
+    _arg("k_pages", k_pages, torch.bfloat16, (rows, G, shape.d))
+    _arg("v_pages", v_pages, torch.bfloat16, (rows, G, shape.d))
+    _arg("k_idx_pages", k_idx_pages, torch.bfloat16, (rows, shape.d_idx), optional=True)
+    _arg("weights", weights, torch.float32, (B, G, pages.max_blocks * 128), optional=True)
+    _arg("weights_out", weights_out, torch.float32, (B, G, new_pages.max_blocks * 128), optional=True)
+    _ws_arg(ws)
+    _require_cuda(kept, k_pages, v_pages, k_idx_pages, weights, weights_out, ws, *getattr(pages, "_keep", ()),
+                  *getattr(new_pages, "_keep", ()))
+    with _on(kept.device, stream) as handle:
+        if weights is not None and weights_out is None:
+            weights_out = torch.empty((B, G, new_pages.max_blocks * 128), dtype=torch.float32, device=kept.device)
+        if ws is None:
+            need = msa_evict_move_workspace_size(shape, pages)
+            if need == 0:
+                raise MsaError("msa_evict_move: shape or paged description rejected")
+            ws = _workspace(need, kept.device)
+        rc = lib.msa_evict_move(ctypes.byref(shape), ctypes.byref(pages), ctypes.byref(new_pages), _ptr(kept),
+                                int(kept.shape[2]), 1 if per_group else 0, _ptr(k_pages), _ptr(v_pages),
+                                _ptr(k_idx_pages), _ptr(weights), _ptr(weights_out), _ptr(ws), _nbytes(ws), handle)
+        _check(rc, "msa_evict_move")
+        if check:
+            _device_check(ws, stream, "msa_evict_move")
+    return weights_out

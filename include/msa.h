@@ -486,6 +486,65 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
                                          float decay, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Eviction from a densely attended layer's paged cache by accumulated
+ * attention weight: which tokens stay under a budget, and their move into
+ * other pages.  (No counterpart on the pages, whose method keeps the whole
+ * cache; this is for the layers of a model that attend densely.)
+ *
+ * msa_evict_select ranks the tokens of every sequence by `weights` (as
+ * msa_dense_attn_decode_paged and msa_attn_weights accumulate them: [batch, G,
+ * max_blocks*128] by position).  A sequence of at most `budget` tokens keeps
+ * all.  Of a longer one the first n_sink and the last n_recent tokens stay, and
+ * the best others up to budget: score descending, ties to the lower position,
+ * NaN last.  per_group == 0: one ranking per sequence, by the sum of the
+ * groups' weights (in 64 bits, rounded once to 32), so that a token stays or
+ * goes with its index key; per_group != 0: each group keeps tokens of its own.
+ *   kept      device int32 [batch, R, budget] (out; R = per_group ? G : 1):
+ *             positions, ascending, padded with -1
+ *   new_lens  device int32 [batch] (out): min(seqlens[b], budget)
+ * Of `pages` only batch, seqlens, max_blocks and max_seqlen count (block_table
+ * is not read).  A length of 0 keeps nothing and is no error; one below 0 or
+ * above max_seqlen is recorded as MSA_ERR_DEVICE_CHECK and treated as 0.
+ * Requires budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget,
+ * weights 16-byte aligned, else MSA_ERR_INVALID_ARG. */
+size_t msa_evict_select_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages, int32_t per_group);
+
+msa_status_t msa_evict_select(const msa_shape_t* shape, const msa_paged_t* pages, const float* weights,
+                              int32_t budget, int32_t n_sink, int32_t n_recent, int32_t per_group, int32_t* kept,
+                              int32_t* new_lens, void* ws, size_t ws_bytes, void* stream);
+
+/* msa_evict_move copies the kept tokens' rows, in kept's order, into the pages
+ * that new_pages names: row i of sequence b (i < new_pages->seqlens[b], usually
+ * msa_evict_select's new_lens) comes from position kept[b, r, i] of `pages`.
+ * Both descriptions are of the same pool (equal num_pages and batch); the old
+ * pages are left as they were, so pages shared between sequences are safe, and
+ * the caller frees them after the call.  A page of new_pages must not belong
+ * to any sequence of `pages` nor appear twice: such a page is recorded as
+ * MSA_ERR_DEVICE_CHECK and nothing is written to it.  (Pages of sequences that
+ * are not in the call are not known to it.)
+ *   k_pages, v_pages      as in the decode calls (read and written)
+ *   k_idx_pages           the index keys' pages, or NULL; with per_group != 0
+ *                         and G > 1 they must be NULL (the groups share them)
+ *   weights, weights_out  both or neither: [batch, G, max_blocks*128] of
+ *                         `pages`, and of new_pages (out): the kept tokens'
+ *                         weights, zeros from the new length on.  They must
+ *                         not overlap.
+ * kept as from msa_evict_select, kept_width its last dimension.  Keys carry
+ * their rotary position in them, so rows are copied as they are.  Rows of the
+ * last new page past the new length are not touched.  Recorded as
+ * MSA_ERR_DEVICE_CHECK, with the row left out: a position outside the sequence,
+ * a page outside the cache; with the sequence treated as empty: a length of
+ * `pages` outside [0, max_seqlen], of new_pages outside [0, min(max_seqlen,
+ * kept_width)].  Pages 16-byte aligned, else MSA_ERR_INVALID_ARG.  Workspace:
+ * 4 bytes per page of the pool. */
+size_t msa_evict_move_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages);
+
+msa_status_t msa_evict_move(const msa_shape_t* shape, const msa_paged_t* pages, const msa_paged_t* new_pages,
+                            const int32_t* kept, int32_t kept_width, int32_t per_group, void* k_pages, void* v_pages,
+                            void* k_idx_pages, const float* weights, float* weights_out, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Work split of the prefill main branch (process-wide; returns the previous
  * value).  This library's own scheduling choice: the pages' kernel runs
  * KV-outer throughout (pnsm.cn sec. 7; yololab.net "KV Outer Gather Q").
@@ -621,7 +680,7 @@ msa_status_t msa_index_topk_decode_noalloc(const msa_shape_t* shape, const msa_v
  * events and returns the summed device time (ms) and launch count of the
  * kernel `name` ("index_topk_prefill", "decode_scan", "decode_select",
  * "sparse_attn", "combine", "count", "plan", "scatter", "dense_attn",
- * "dense_decode", ...).
+ * "dense_decode", "evict_select", "evict_move", ...).
  * With name == NULL it returns the number of kernels launched since the last
  * msa_profile_reset (launches are counted even while timing is disabled). */
 msa_status_t msa_profile_enable(int on);
@@ -648,6 +707,9 @@ msa_status_t msa_profile_read(const char* kernel, double* total_ms, int64_t* cou
  *   221      bounded-wait self-test              231  decode candidate merge
  *   241      dense paged decode (a length, info0 = sequence, info1 = length; a
  *            page, info0 = sequence, info1 = block; a wait)
+ *   261      eviction's choice (info0 = sequence, info1 = length)
+ *   271      eviction's move (info0 = sequence; info1 = a length, a row of
+ *            kept, or a block)
  * MSA_ERR_TIMEOUT codes come from a bounded wait that ran out (about a
  * second); the call's results are then not valid, the context still is. */
 msa_status_t msa_get_device_error(void* ws, int32_t* code, int32_t* where, int32_t* info0,
