@@ -19,8 +19,8 @@ constexpr int32_t kSiteAttnWeights = 251;   // key weights of a prompt's queries
 constexpr int32_t kSiteEvictSelect = 261;   // a length outside its bounds
 constexpr int32_t kSiteEvictMove = 271;     // lengths, kept indices and pages of the move
 
-// CTAs of the dense paged decode (one per SM of a B200; fewer on a smaller
-// device).  A constant, so that the workspace size needs no device.
+// CTAs of the dense paged decode and of the key weights (one per SM of a B200;
+// fewer on a smaller device).  A constant, so that the workspace size needs no device.
 constexpr int kDecodeCtas = 148;
 
 struct DenseDecodeArgs {
@@ -50,6 +50,27 @@ struct DenseDecodeLayout {
 };
 DenseDecodeLayout dense_decode_layout(int32_t batch, int32_t H, int32_t d, int32_t max_seqlen, bool with_weights);
 int launch_dense_decode(const DenseDecodeArgs& a, void* stream);
+
+struct AttnWeightsArgs {
+  const void* q;              // bf16 [total_q, H, d]
+  const void* k;              // bf16 [total_k, G, d]
+  const float* lse;           // [total_q, H]
+  float* weights;             // [batch, G, width]
+  int64_t width;
+  float decay, sm_scale;
+  int32_t batch, H, G, d;
+  const int32_t *cu_q, *cu_k;
+  int64_t total_q, total_k;
+  DevError* err;
+  // workspace slices (attn_weights_layout)
+  void* open;                 // [CTA]: the key block that a CTA leaves to be joined
+  float* part;                // [CTA, 2, 256]
+};
+struct AttnWeightsLayout {
+  size_t open, part, total;
+};
+AttnWeightsLayout attn_weights_layout();
+int launch_attn_weights(const AttnWeightsArgs& a, void* stream);
 
 struct EvictSelectArgs {
   const float* weights;       // [batch, G, width]

@@ -61,6 +61,36 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
   return launch_dense_decode(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
 }
 
+size_t msa_attn_weights_workspace_size(const msa_shape_t* shape, const msa_varlen_t* seqs) {
+  if (check_shape(shape) != MSA_OK || check_seqs(seqs) != MSA_OK) return 0;
+  return attn_weights_layout().total;
+}
+
+msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs, const void* q, const void* k,
+                              const float* lse, float* weights, int64_t width, float decay, void* ws, size_t ws_bytes,
+                              void* stream) {
+  msa_status_t st = check_shape(shape);
+  if (st != MSA_OK) return st;
+  st = check_seqs(seqs);
+  if (st != MSA_OK) return st;
+  if (width < seqs->max_k_len || !decay_ok(decay)) return MSA_ERR_INVALID_ARG;
+  if (seqs->total_q > 0 && (!q || !k || !lse || !weights)) return MSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16)) return MSA_ERR_INVALID_ARG;
+  const AttnWeightsLayout L = attn_weights_layout();
+  if (!ws_ok(ws, ws_bytes, L.total)) return MSA_ERR_WORKSPACE;
+  if (!clear_error(ws, stream)) return MSA_ERR_CUDA;
+  if (seqs->total_q == 0) return MSA_OK;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  AttnWeightsArgs a{};
+  a.q = q; a.k = k; a.lse = lse; a.weights = weights; a.width = width; a.decay = decay;
+  a.sm_scale = shape->sm_scale; a.batch = seqs->batch; a.H = shape->H; a.G = shape->G; a.d = shape->d;
+  a.cu_q = seqs->cu_q; a.cu_k = seqs->cu_k; a.total_q = seqs->total_q; a.total_k = seqs->total_k;
+  a.err = static_cast<DevError*>(ws);
+  a.open = base + L.open;
+  a.part = reinterpret_cast<float*>(base + L.part);
+  return launch_attn_weights(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
+}
+
 size_t msa_evict_select_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages, int32_t per_group) {
   if (check_paged(shape, pages) != MSA_OK) return 0;
   return kWsHeader + evict_select_keys_bytes(pages->batch, per_group != 0 ? shape->G : 1, pages->max_seqlen);

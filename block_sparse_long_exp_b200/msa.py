@@ -59,6 +59,7 @@ EXPORTED = [
     "msa_prefill_workspace_size", "msa_prefill", "msa_set_prefill_overlap", "msa_index_kl_workspace_size",
     "msa_sparse_attn_backward_workspace_size",
     "msa_dense_attn_decode_paged_workspace_size", "msa_dense_attn_decode_paged",
+    "msa_attn_weights_workspace_size", "msa_attn_weights",
     "msa_evict_select_workspace_size", "msa_evict_select", "msa_evict_move_workspace_size", "msa_evict_move",
 ]
 
@@ -182,6 +183,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.msa_dense_attn_decode_paged_workspace_size.restype = sz
     lib.msa_dense_attn_decode_paged.argtypes = [P(Shape), P(Paged), vp, vp, vp, vp, vp, vp, f32, vp, sz, vp]
     lib.msa_dense_attn_decode_paged.restype = i32
+    lib.msa_attn_weights_workspace_size.argtypes = [P(Shape), P(Varlen)]
+    lib.msa_attn_weights_workspace_size.restype = sz
+    lib.msa_attn_weights.argtypes = [P(Shape), P(Varlen), vp, vp, vp, vp, i64, f32, vp, sz, vp]
+    lib.msa_attn_weights.restype = i32
     lib.msa_evict_select_workspace_size.argtypes = [P(Shape), P(Paged), i32]
     lib.msa_evict_select_workspace_size.restype = sz
     lib.msa_evict_select.argtypes = [P(Shape), P(Paged), vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
@@ -1062,6 +1067,47 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
         if check:
             _device_check(ws, stream, "msa_dense_attn_decode_paged")
     return out, lse
+
+
+def msa_attn_weights_workspace_size(shape: Shape, seqs: Varlen) -> int:
+    """Workspace bytes of msa_attn_weights (0: rejected)."""
+    return load_library().msa_attn_weights_workspace_size(ctypes.byref(shape), ctypes.byref(seqs))
+
+
+def msa_attn_weights(shape: Shape, seqs: Varlen, q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
+                     weights: Optional[torch.Tensor] = None, decay: float = 1.0, ws: Optional[torch.Tensor] = None,
+                     stream=None, check: bool = True) -> torch.Tensor:
+    """Adds the attention weight that the queries (each sequence's last T_b
+    tokens) give every key: weights f32 [batch, G, width >= max S_b] becomes
+    decay * weights + sum over queries and the group's heads of exp(s - lse),
+    lse [total_q, H] from msa_dense_attn.  weights=None starts from zeros of
+    width max S_b.  Returns weights."""
+    lib = load_library()
+    B, G = seqs.batch, shape.G
+    _arg("q", q, torch.bfloat16, (seqs.total_q, shape.H, shape.d))
+    _arg("k", k, torch.bfloat16, (seqs.total_k, G, shape.d))
+    _arg("lse", lse, torch.float32, (seqs.total_q, shape.H))
+    _arg("weights", weights, torch.float32, optional=True)
+    if weights is not None and (weights.dim() != 3 or tuple(weights.shape[:2]) != (B, G) or
+                                weights.shape[2] < seqs.max_k_len):
+        raise MsaError(f"weights: shape {tuple(weights.shape)}, expected ({B}, {G}, {seqs.max_k_len} or more)")
+    decay = _decay(decay)
+    _ws_arg(ws)
+    _require_cuda(q, k, lse, weights, ws, *getattr(seqs, "_keep", ()))
+    with _on(q.device, stream) as handle:
+        if weights is None:
+            weights = torch.zeros((B, G, seqs.max_k_len), dtype=torch.float32, device=q.device)
+        if ws is None:
+            need = msa_attn_weights_workspace_size(shape, seqs)
+            if need == 0:
+                raise MsaError("msa_attn_weights: shape or sequence description rejected")
+            ws = _workspace(need, q.device)
+        rc = lib.msa_attn_weights(ctypes.byref(shape), ctypes.byref(seqs), _ptr(q), _ptr(k), _ptr(lse), _ptr(weights),
+                                  int(weights.shape[2]), decay, _ptr(ws), _nbytes(ws), handle)
+        _check(rc, "msa_attn_weights")
+        if check:
+            _device_check(ws, stream, "msa_attn_weights")
+    return weights
 
 
 def msa_evict_select_workspace_size(shape: Shape, pages: Paged, per_group: bool = False) -> int:

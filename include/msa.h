@@ -486,6 +486,30 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
                                          float decay, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* The attention weight that a prompt's queries give every key, beside
+ * msa_dense_attn, whose lse it takes: what msa_dense_attn_decode_paged adds up
+ * for one new token, for the T_b queries of each sequence (all of a prompt, or an
+ * observation window: the last tokens alone, with their q and lse):
+ *   weights[b, g, j] = decay weights[b, g, j] + sum over the queries at positions
+ *                      >= j and the group's heads of exp(sm_scale <q, k_j> - lse)
+ * for j < S_b (decay in [0, 1], applied once per call; with 0 the old value is
+ * not read).  weights is f32 [batch, G, width], by position; entries from S_b on
+ * are not touched, nor is a sequence without queries.  A (query, head) whose lse
+ * is -inf has seen no key and adds nothing.  width >= max_k_len (a paged cache's
+ * max_blocks * 128, so that decode steps go on from it), q, k and lse 16-byte
+ * aligned, else MSA_ERR_INVALID_ARG.  A sequence with more queries than keys is
+ * recorded as MSA_ERR_DEVICE_CHECK and left as it is.  Sums are 32-bit and in a
+ * fixed order: the same from run to run (on one device model). */
+size_t msa_attn_weights_workspace_size(const msa_shape_t* shape, const msa_varlen_t* seqs);
+
+msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs,
+                              const void* q,      /* device bf16 [total_q, H, d] */
+                              const void* k,      /* device bf16 [total_k, G, d] */
+                              const float* lse,   /* device f32 [total_q, H] */
+                              float* weights,     /* device f32 [batch, G, width] (in / out) */
+                              int64_t width, float decay, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Eviction from a densely attended layer's paged cache by accumulated
  * attention weight: which tokens stay under a budget, and their move into
  * other pages.  (No counterpart on the pages, whose method keeps the whole
@@ -680,7 +704,7 @@ msa_status_t msa_index_topk_decode_noalloc(const msa_shape_t* shape, const msa_v
  * events and returns the summed device time (ms) and launch count of the
  * kernel `name` ("index_topk_prefill", "decode_scan", "decode_select",
  * "sparse_attn", "combine", "count", "plan", "scatter", "dense_attn",
- * "dense_decode", "evict_select", "evict_move", ...).
+ * "dense_decode", "attn_weights", "evict_select", "evict_move", ...).
  * With name == NULL it returns the number of kernels launched since the last
  * msa_profile_reset (launches are counted even while timing is disabled). */
 msa_status_t msa_profile_enable(int on);
@@ -707,6 +731,7 @@ msa_status_t msa_profile_read(const char* kernel, double* total_ms, int64_t* cou
  *   221      bounded-wait self-test              231  decode candidate merge
  *   241      dense paged decode (a length, info0 = sequence, info1 = length; a
  *            page, info0 = sequence, info1 = block; a wait)
+ *   251      key weights of a prompt (info0 = sequence, info1 = T_b; a wait)
  *   261      eviction's choice (info0 = sequence, info1 = length)
  *   271      eviction's move (info0 = sequence; info1 = a length, a row of
  *            kept, or a block)
