@@ -7,7 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <vector_types.h>
+#include <atomic>
+
+#include <cuda_runtime.h>
 
 namespace msa {
 
@@ -23,6 +25,20 @@ constexpr int32_t kSiteEvictMove = 271;     // lengths, kept indices and pages o
 // fewer on a smaller device).  A constant, so that the workspace size needs no device.
 constexpr int kDecodeCtas = 148;
 
+// A kernel's dynamic shared memory allowed once per device (`done`: a bit per
+// device; the call takes 1 us).
+template <typename K>
+int allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0 && (done->load(std::memory_order_acquire) & bit) != 0) return 0;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return (int)e;
+}
+
 struct DenseDecodeArgs {
   const void* q;              // bf16 [batch, H, d]
   const void* k_pages;        // bf16 [num_pages * 128, G, d]
@@ -37,16 +53,16 @@ struct DenseDecodeArgs {
   const int32_t* block_table; // [batch, max_blocks]
   int32_t max_blocks, max_seqlen;
   int64_t num_pages;
-  DevError* err;
+  DevError* err;              // written by the join
   // workspace slices (dense_decode_layout)
-  int32_t* seq_start;         // [batch + 1]: first tile of each sequence; [batch]: tiles in all
+  DevError* errors;           // [CTA]
   float2* stats;              // [batch, H]: maximum and sum of each head's softmax
   float2* part_ml;            // [CTA, 2, H]
   float* part_o;              // [CTA, 2, H, d]
   float* logits;              // scores of every key (with weights only)
 };
 struct DenseDecodeLayout {
-  size_t seq_start, stats, part_ml, part_o, logits, total;
+  size_t errors, stats, part_ml, part_o, logits, total;
 };
 DenseDecodeLayout dense_decode_layout(int32_t batch, int32_t H, int32_t d, int32_t max_seqlen, bool with_weights);
 int launch_dense_decode(const DenseDecodeArgs& a, void* stream);

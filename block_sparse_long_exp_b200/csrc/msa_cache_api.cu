@@ -44,7 +44,6 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
   const DenseDecodeLayout L =
       dense_decode_layout(pages->batch, shape->H, shape->d, pages->max_seqlen, weights != nullptr);
   if (!ws_ok(ws, ws_bytes, L.total)) return MSA_ERR_WORKSPACE;
-  if (!clear_error(ws, stream)) return MSA_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
   DenseDecodeArgs a{};
   a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.out = out; a.lse = lse;
@@ -53,7 +52,7 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
   a.seqlens = pages->seqlens; a.block_table = pages->block_table;
   a.max_blocks = pages->max_blocks; a.max_seqlen = pages->max_seqlen; a.num_pages = pages->num_pages;
   a.err = reinterpret_cast<DevError*>(ws);
-  a.seq_start = reinterpret_cast<int32_t*>(base + L.seq_start);
+  a.errors = reinterpret_cast<DevError*>(base + L.errors);
   a.stats = reinterpret_cast<float2*>(base + L.stats);
   a.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
   a.part_o = reinterpret_cast<float*>(base + L.part_o);

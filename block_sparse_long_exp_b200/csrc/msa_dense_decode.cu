@@ -31,6 +31,8 @@
 //           Reading K again would cost 2 G d.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "msa_common.cuh"
 #include "msa_cache.h"
 #include "msa_internal.h"
@@ -49,15 +51,18 @@ template <int D>
 __host__ __device__ constexpr int stage_bytes() { return 2 * 64 * D * 2; }          // keys and values of one tile
 template <int D>
 __host__ __device__ constexpr int num_stages() { return D == 128 ? 6 : 10; }
+// Half the output fragments of four warps: the sums are merged in two halves of the columns, which leaves the
+// join's first CTAs room beside this kernel's (they are in place when it ends).
 template <int D>
-__host__ __device__ constexpr int merge_bytes() { return 4 * 16 * D * 4; }          // four warps' output fragments
+__host__ __device__ constexpr int merge_bytes() { return 4 * 16 * (D / 2) * 4; }
 
 struct DecCtl {
-  uint64_t full[16];
-  uint64_t empty[16];
-  int32_t valid[16];            // tokens of the tile to attend (0: its page is outside the cache)
-  int32_t warp_sum[16];
+  uint64_t full[10];
+  uint64_t empty[10];
+  int32_t valid[10];            // tokens of the tile to attend (0: its page is outside the cache)
+  int32_t warp_sum[10];
   int32_t first_seq, first_start, total;
+  int32_t lens[kDecThreads];    // the batch's lengths, where a thread has one at most
   float ml[4][2][16];           // (m, l) rows of the merging warps
 };
 
@@ -97,12 +102,13 @@ __device__ __forceinline__ int run_of(int t, int total, int n) {
   return t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q;
 }
 
-// The lengths of the batch, read 32 at a time by a whole warp.
+// The lengths of the batch: from shared memory where they fit, else read 32 at a time by a whole warp.
 struct SeqLens {
-  const int32_t* p;
+  const int32_t *p, *near;
   int batch, max_seqlen, base, mine;
-  __device__ SeqLens(const int32_t* lens, int batch_, int max_, int at) : p(lens), batch(batch_), max_seqlen(max_) {
-    fetch(at);
+  __device__ SeqLens(const int32_t* lens, const int32_t* smem, int batch_, int max_, int at)
+      : p(lens), near(smem), batch(batch_), max_seqlen(max_), base(0), mine(0) {
+    if (batch > kDecThreads) fetch(at);
   }
   __device__ void fetch(int at) {
     const int i = at + (threadIdx.x & 31);
@@ -110,6 +116,7 @@ struct SeqLens {
     mine = i < batch ? seq_len(p[i], max_seqlen) : 0;
   }
   __device__ int operator()(int b) {
+    if (batch <= kDecThreads) return near[b];
     if (b - base >= 32) fetch(b);
     return __shfl_sync(0xffffffffu, mine, b - base);
   }
@@ -121,8 +128,8 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                     int batch, int H, int G, float sm_scale, const int32_t* __restrict__ seqlens,
                     const int32_t* __restrict__ block_table, int max_blocks, int max_seqlen, int64_t num_pages,
-                    int32_t* __restrict__ seq_start, float2* __restrict__ stats, float2* __restrict__ part_ml,
-                    float* __restrict__ part_o, float* __restrict__ logits, int logit_tiles, DevError* err) {
+                    float2* __restrict__ stats, float2* __restrict__ part_ml, float* __restrict__ part_o,
+                    float* __restrict__ logits, int logit_tiles, DevError* errors) {
   constexpr int NST = num_stages<D>();
   constexpr int STAGE = stage_bytes<D>();
   constexpr int KV = STAGE / 2;
@@ -137,16 +144,23 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const int Hg = H / G;
   const int tok = 64 / G;                       // tokens per tile
   pdl_launch_dependents();                      // the join waits for this grid's end by itself
+  DevError* err = errors + blockIdx.x;          // the join makes one word of them
 
   // ---- this CTA's run of tiles: one scan over the batch's lengths
   {
+    if (threadIdx.x == 0) {
+      *err = DevError{0, 0, 0, 0};
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
     const int per = (batch + kDecThreads - 1) / kDecThreads;
     const int b0 = threadIdx.x * per;
-    int sum = 0;
+    int sum = 0, bad = -1;
     for (int b = b0; b < min(b0 + per, batch); ++b) {
       const int raw_len = seqlens[b];
       const int L = seq_len(raw_len, max_seqlen);
-      if (blockIdx.x == 0 && L != raw_len) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteDenseDecode, b, raw_len);
+      if (L != raw_len) bad = b;
+      if (per == 1) ctl->lens[b] = L;
       sum += (L + tok - 1) / tok;
     }
     int incl = sum;
@@ -164,6 +178,7 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       fence_mbar_init();
     }
     __syncthreads();
+    if (blockIdx.x == 0 && bad >= 0) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteDenseDecode, bad, seqlens[bad]);
     int before = 0, total = 0;
     for (int w = 0; w <= kComputeWarps; ++w) {
       if (w < warp) before += ctl->warp_sum[w];
@@ -181,25 +196,18 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       ctl->first_seq = b;
       ctl->first_start = s;
     }
-    if (threadIdx.x == 0) {
-      ctl->total = total;
-      if (blockIdx.x == 0) seq_start[batch] = total;
-    }
+    if (threadIdx.x == 0) ctl->total = total;
     __syncthreads();
   }
   const int total = ctl->total;
   const int lo = run_start(blockIdx.x, total, gridDim.x);
   const int hi = run_start(blockIdx.x + 1, total, gridDim.x);
   if (lo >= hi) return;
-  SeqLens lens(seqlens, batch, max_seqlen, ctl->first_seq);
+  SeqLens lens(seqlens, ctl->lens, batch, max_seqlen, ctl->first_seq);
   int b = ctl->first_seq, s = ctl->first_start;      // the sequence at hand and its first tile
 
   if (warp == kComputeWarps) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
     bool ok = true;
     int issued = 0;
     for (int t = lo; t < hi;) {
@@ -402,47 +410,50 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
     const int part = set * nsub + sub;            // of kSets * nsub parts of group g
     for (int step = kSets * nsub / 2; step >= 1; step >>= 1) {
-      if (part >= step && part < 2 * step) {
-        const int slot = (part - step) * G + g;
-        float* dst = mbuf + slot * (16 * D);
+      const bool gives = part >= step && part < 2 * step, takes = part < step;
+      const int slot = (gives ? part - step : part) * G + g;
+      float* buf = mbuf + slot * (16 * (D / 2));
+      float fa[2] = {0.f, 0.f}, fb[2] = {0.f, 0.f};
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+      for (int half = 0; half < 2; ++half) {
+        if (gives) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) dst[(4 * n + x) * 32 + lane] = o[n][x];
-        if ((lane & 3) == 0) {
+          for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            ctl->ml[slot][0][r + 8 * y] = m[y];
-            ctl->ml[slot][1][r + 8 * y] = l[y];
+            for (int x = 0; x < 4; ++x) buf[(4 * n + x) * 32 + lane] = o[half * (D / 16) + n][x];
+          if (half == 0 && (lane & 3) == 0) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              ctl->ml[slot][0][r + 8 * y] = m[y];
+              ctl->ml[slot][1][r + 8 * y] = l[y];
+            }
           }
         }
-      }
-      compute_bar();
-      if (part < step) {
-        const int slot = part * G + g;
-        const float* src = mbuf + slot * (16 * D);
-        float fa[2], fb[2];
+        compute_bar();
+        if (takes) {
+          if (half == 0) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float m2 = ctl->ml[slot][0][r + 8 * y], l2 = ctl->ml[slot][1][r + 8 * y];
-          const float mn = fmaxf(m[y], m2);
-          const float ms = mn == -INFINITY ? 0.f : mn;
-          fa[y] = ex2_approx(m[y] - ms);
-          fb[y] = ex2_approx(m2 - ms);
-          l[y] = l[y] * fa[y] + l2 * fb[y];
-          m[y] = mn;
+            for (int y = 0; y < 2; ++y) {
+              const float m2 = ctl->ml[slot][0][r + 8 * y], l2 = ctl->ml[slot][1][r + 8 * y];
+              const float mn = fmaxf(m[y], m2);
+              const float ms = mn == -INFINITY ? 0.f : mn;
+              fa[y] = ex2_approx(m[y] - ms);
+              fb[y] = ex2_approx(m2 - ms);
+              l[y] = l[y] * fa[y] + l2 * fb[y];
+              m[y] = mn;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              o[half * (D / 16) + n][x] = o[half * (D / 16) + n][x] * fa[x >> 1] + buf[(4 * n + x) * 32 + lane] * fb[x >> 1];
         }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            o[n][x] = o[n][x] * fa[x >> 1] + src[(4 * n + x) * 32 + lane] * fb[x >> 1];
+        compute_bar();
       }
-      compute_bar();
     }
     if (part == 0) {
       const bool whole = t0 == s && e == s + nt;
-      if (t0 == s && warp == 0 && lane == 0) seq_start[b] = s;
       const int slot = t0 == s ? 1 : 0;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -474,85 +485,175 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
 }
 
-// Joins the parts of the sequences that lie in several CTAs' runs, one (b, h)
-// per WPJ warps, and writes the rows of sequences without tokens.
-template <int D, int WPJ>
+// Joins the parts of the sequences that lie in several CTAs' runs, writes the
+// rows of sequences without tokens, and makes one error word of the CTAs'.  WPJ
+// warps have one (b, h) and VEC columns a lane, so that few sequences in many
+// parts and many in few parts both keep the loads in flight: a warp reads the
+// parts w, w + WPJ, ... eight at a time.
+constexpr int kMaxParts = (kDecodeCtas + 31) / 32 * 32;
+template <int D, int WPJ, int VEC>
 __global__ void __launch_bounds__(256)
 dense_join_kernel(__nv_bfloat16* __restrict__ out, float* __restrict__ lse, int batch, int H, int G,
-                  const int32_t* __restrict__ seqlens, int max_seqlen, const int32_t* __restrict__ seq_start,
-                  const float2* __restrict__ part_ml, const float* __restrict__ part_o, float2* __restrict__ stats,
-                  int ctas) {
+                  const int32_t* __restrict__ seqlens, int max_seqlen, const float2* __restrict__ part_ml,
+                  const float* __restrict__ part_o, float2* __restrict__ stats, int ctas,
+                  const DevError* __restrict__ errors, DevError* __restrict__ err) {
   constexpr int JPC = 8 / WPJ;                   // (b, h) pairs per CTA
-  constexpr int VEC = D / 32;                    // columns per lane
-  __shared__ float acc[WPJ > 1 ? 8 : 1][D];
-  __shared__ float sml[2][8];
+  constexpr int CB = D / (32 * VEC);             // CTAs that share a pair's columns
+  constexpr int BATCH = 8;                       // parts in flight per warp
+  __shared__ float acc[WPJ > 1 ? 8 : 1][32 * VEC];
+  __shared__ float fac[JPC][kMaxParts];
+  __shared__ int32_t wsum[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = warp % WPJ;
-  const int64_t pair = (int64_t)blockIdx.x * JPC + warp / WPJ;
-  pdl_wait();
-  // with WPJ > 1 every warp of a CTA has the same pair, so the exits are the CTA's
-  if (pair >= (int64_t)batch * H) return;
-  const int b = (int)(pair / H), h = (int)(pair - (int64_t)b * H);
+  const int tok = 64 / G;
+  pdl_launch_dependents();
+  // ---- the first tile of the CTA's first sequence, and all tiles (before the kernel ahead has ended: lengths are
+  // no output of it)
+  const int64_t pair0 = (int64_t)(blockIdx.x / CB) * JPC;
+  const int b0 = (int)(pair0 / H);
+  int total, s;
+  {
+    int sum = 0, mine = 0;
+    for (int i = threadIdx.x; i < batch; i += 256) {
+      const int n = (seq_len(seqlens[i], max_seqlen) + tok - 1) / tok;
+      sum += n;
+      if (i < b0) mine += n;
+    }
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      mine += __shfl_xor_sync(0xffffffffu, mine, x);
+    }
+    if (lane == 0) {
+      wsum[0][warp] = sum;
+      wsum[1][warp] = mine;
+    }
+    __syncthreads();
+    total = 0;
+    s = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      total += wsum[0][x];
+      s += wsum[1][x];
+    }
+  }
+  const int64_t pair = pair0 + warp / WPJ;
+  const int col = (int)(blockIdx.x % CB) * 32 * VEC + VEC * lane;
+  const bool live = pair < (int64_t)batch * H;
+  const int b = live ? (int)(pair / H) : b0, h = (int)(pair - (int64_t)b * H);
+  for (int i = b0; i < b; ++i) s += (seq_len(seqlens[i], max_seqlen) + tok - 1) / tok;
   const int L = seq_len(seqlens[b], max_seqlen);
-  if (L == 0) {
+  const int nt = (L + tok - 1) / tok;
+  const int c0 = L > 0 ? run_of(s, total, ctas) : 0, n = L > 0 ? run_of(s + nt - 1, total, ctas) - c0 + 1 : 0;
+  pdl_wait();
+  if (blockIdx.x == 0 && warp == 0) {            // the first CTA's that found something
+    int first = ctas;
+    for (int i = lane; i < ctas; i += 32)
+      if (errors[i].code != 0) first = min(first, i);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) *err = first < ctas ? errors[first] : DevError{0, 0, 0, 0};
+  }
+  // with WPJ > 1 every warp of a CTA has the same pair, so the exits are the CTA's
+  if (!live || n == 1) return;                   // written by its CTA
+  __nv_bfloat16* dst = out + pair * D + col;
+  auto store = [&](const float (&y)[VEC]) {
+    if constexpr (VEC == 1) {
+      dst[0] = __float2bfloat16_rn(y[0]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < VEC; x += 2) reinterpret_cast<uint32_t*>(dst)[x / 2] = pack_bf16x2(y[x], y[x + 1]);
+    }
+  };
+  float o[VEC];
+#pragma unroll
+  for (int x = 0; x < VEC; ++x) o[x] = 0.f;
+  if (n == 0) {
     if (w == 0) {
-      for (int x = lane; x < D / 2; x += 32) reinterpret_cast<uint32_t*>(out + pair * D)[x] = 0u;
-      if (lane == 0) {
+      store(o);
+      if (lane == 0 && blockIdx.x % CB == 0) {
         if (lse != nullptr) lse[pair] = -INFINITY;
         stats[pair] = make_float2(-INFINITY, 0.f);
       }
     }
     return;
   }
-  const int tok = 64 / G, nt = (L + tok - 1) / tok;
-  const int total = seq_start[batch], s = seq_start[b];
-  const int c0 = run_of(s, total, ctas), c1 = run_of(s + nt - 1, total, ctas);
-  if (c0 == c1) return;                          // written by its CTA
-  // the part of CTA i: slot 1 where its run holds the sequence's first tile
-  auto at_of = [&](int i) -> int64_t { return ((int64_t)i * 2 + (i == c0 ? 1 : 0)) * H + h; };
-  float m = -INFINITY;
-  for (int i = c0 + lane; i <= c1; i += 32) m = fmaxf(m, part_ml[at_of(i)].x);
+  // the part of CTA c0 + i: slot 1 where its run holds the sequence's first tile
+  auto at_of = [&](int i) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * H + h; };
+  float v[BATCH][VEC];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + u * WPJ;
+#pragma unroll
+      for (int x = 0; x < VEC; ++x) v[u][x] = 0.f;
+      if (i < n) {
+        const float* src = part_o + at_of(i) * D + col;
+        if constexpr (VEC == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(src);
+          v[u][0] = q.x; v[u][1] = q.y; v[u][2] = q.z; v[u][3] = q.w;
+        } else if constexpr (VEC == 2) {
+          const float2 q = *reinterpret_cast<const float2*>(src);
+          v[u][0] = q.x; v[u][1] = q.y;
+        } else {
+          v[u][0] = *src;
+        }
+      }
+    }
+  };
+  fetch(w);
+  // every warp: the maximum, the sum and each part's factor
+  float2 ml[kMaxParts / 32];
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int x = 0; x < kMaxParts / 32; ++x) {
+    const int i = 32 * x + lane;
+    ml[x] = i < n ? part_ml[at_of(i)] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, ml[x].x);
+  }
 #pragma unroll
   for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ms = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[VEC];
+  float* f = fac[warp / WPJ];
 #pragma unroll
-  for (int x = 0; x < VEC; ++x) o[x] = 0.f;
-#pragma unroll 4
-  for (int i = c0 + w; i <= c1; i += WPJ) {
-    const int64_t at = at_of(i);
-    const float2 ml = part_ml[at];
-    const float f = ex2_approx(ml.x - ms);
-    l = fmaf(ml.y, f, l);
-    if constexpr (VEC == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(part_o + at * D + 4 * lane);
-      o[0] = fmaf(v.x, f, o[0]); o[1] = fmaf(v.y, f, o[1]); o[2] = fmaf(v.z, f, o[2]); o[3] = fmaf(v.w, f, o[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(part_o + at * D + 2 * lane);
-      o[0] = fmaf(v.x, f, o[0]); o[1] = fmaf(v.y, f, o[1]);
+  for (int x = 0; x < kMaxParts / 32; ++x) {
+    const float e = ex2_approx(ml[x].x - ms);
+    l = fmaf(ml[x].y, e, l);
+    f[32 * x + lane] = e;                        // the warps of a pair write the same
+  }
+#pragma unroll
+  for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  __syncwarp();
+  for (int i0 = w;;) {
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int i = i0 + u * WPJ;
+      if (i < n) {
+        const float e = f[i];
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) o[x] = fmaf(v[u][x], e, o[x]);
+      }
     }
+    i0 += BATCH * WPJ;
+    if (i0 >= n) break;
+    fetch(i0);
   }
   if constexpr (WPJ > 1) {
-    if (lane == 0) sml[0][warp] = l;
 #pragma unroll
     for (int x = 0; x < VEC; ++x) acc[warp][VEC * lane + x] = o[x];
     __syncthreads();
     if (w != 0) return;
-    l = 0.f;
 #pragma unroll
-    for (int x = 0; x < VEC; ++x) o[x] = 0.f;
+    for (int x = 0; x < VEC; ++x) {
+      o[x] = 0.f;
 #pragma unroll
-    for (int u = 0; u < WPJ; ++u) {
-      l += sml[0][u];
-#pragma unroll
-      for (int x = 0; x < VEC; ++x) o[x] += acc[u][VEC * lane + x];
+      for (int u = 0; u < WPJ; ++u) o[x] += acc[u][VEC * lane + x];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(out + pair * D) + lane * (VEC / 2);
 #pragma unroll
-  for (int x = 0; x < VEC / 2; ++x) dst[x] = pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
-  if (lane == 0) {
+  for (int x = 0; x < VEC; ++x) o[x] *= inv;
+  store(o);
+  if (lane == 0 && blockIdx.x % CB == 0) {
     if (lse != nullptr) lse[pair] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     stats[pair] = make_float2(m, l);
   }
@@ -620,15 +721,16 @@ template <int D, bool kWeights>
 int launch_split(const DenseDecodeArgs& a, int ctas, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                  int logit_tiles, cudaStream_t st) {
   constexpr int smem = 1024 + num_stages<D>() * stage_bytes<D>() + merge_bytes<D>() + (int)sizeof(DecCtl);
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<D, kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem);
-  if (e != cudaSuccess) return (int)e;
+  static_assert(smem <= 220 * 1024, "shared memory of one CTA, and 7 KB for the join's beside it");
+  static_assert(num_stages<D>() <= 10, "barriers of the stages");
+  static std::atomic<uint64_t> ready{0};
+  const int rc = allow_smem(dense_decode_kernel<D, kWeights>, smem, &ready);
+  if (rc != 0) return rc;
   ProfScope p("dense_decode", st);
   dense_decode_kernel<D, kWeights><<<ctas, kDecThreads, smem, st>>>(
       tm_k, tm_v, static_cast<const __nv_bfloat16*>(a.q), static_cast<__nv_bfloat16*>(a.out), a.lse, a.batch, a.H, a.G,
-      a.sm_scale, a.seqlens, a.block_table, a.max_blocks, a.max_seqlen, a.num_pages, a.seq_start, a.stats, a.part_ml,
-      a.part_o, a.logits, logit_tiles, a.err);
+      a.sm_scale, a.seqlens, a.block_table, a.max_blocks, a.max_seqlen, a.num_pages, a.stats, a.part_ml, a.part_o,
+      a.logits, logit_tiles, a.errors);
   return (int)cudaGetLastError();
 }
 
@@ -660,7 +762,7 @@ DenseDecodeLayout dense_decode_layout(int32_t batch, int32_t H, int32_t d, int32
     off = align_up(off + bytes, 256);
     return o;
   };
-  L.seq_start = take(sizeof(int32_t) * ((size_t)batch + 1));
+  L.errors = take(sizeof(DevError) * kDecodeCtas);
   L.stats = take(sizeof(float2) * (size_t)batch * H);
   L.part_ml = take(sizeof(float2) * (size_t)kDecodeCtas * 2 * H);
   L.part_o = take(sizeof(float) * (size_t)kDecodeCtas * 2 * H * d);
@@ -699,16 +801,16 @@ int launch_dense_decode(const DenseDecodeArgs& a, void* stream) {
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   {
     ProfScope p("dense_join", stream);
-    // few sequences lie in many runs each: eight warps to a (b, h); many lie in few: one
-    const bool wide = a.batch <= 16;
-    const dim3 grid((unsigned)(wide ? pairs : (pairs + 7) / 8));
-#define MSA_JOIN(DD, W)                                                                                         \
-  rc = launch_after(dense_join_kernel<DD, W>, grid, 256, st, out, a.lse, a.batch, a.H, a.G, a.seqlens,             \
-                    a.max_seqlen, a.seq_start, a.part_ml, a.part_o, a.stats, ctas)
+    // few sequences lie in many runs each: eight warps to a (b, h), and up to two sequences its columns over 2 or 4
+    // CTAs (1 x 1M tokens: JOINWIDE us against JOINMID); many lie in few: one warp
+#define MSA_JOIN(DD, W, VEC)                                                                                       \
+  rc = launch_after(dense_join_kernel<DD, W, VEC>,                                                                 \
+                    dim3((unsigned)((pairs + 8 / W - 1) / (8 / W) * (DD / (32 * VEC)))), 256, st, out, a.lse, a.batch,     \
+                    a.H, a.G, a.seqlens, a.max_seqlen, a.part_ml, a.part_o, a.stats, ctas, a.errors, a.err)
     if (a.d == 128) {
-      if (wide) MSA_JOIN(128, 8); else MSA_JOIN(128, 1);
+      if (a.batch <= 2) MSA_JOIN(128, 8, 1); else if (a.batch <= 16) MSA_JOIN(128, 8, 4); else MSA_JOIN(128, 1, 4);
     } else {
-      if (wide) MSA_JOIN(64, 8); else MSA_JOIN(64, 1);
+      if (a.batch <= 2) MSA_JOIN(64, 8, 1); else if (a.batch <= 16) MSA_JOIN(64, 8, 2); else MSA_JOIN(64, 1, 2);
     }
 #undef MSA_JOIN
   }

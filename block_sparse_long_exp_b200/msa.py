@@ -264,12 +264,13 @@ def _require_cuda(*ts: Optional[torch.Tensor]):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()                           # -1 on the CPU
+        if at < 0:
             raise MsaError("the MSA kernels need CUDA tensors (no CPU path exists)")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise MsaError(f"tensors on different devices ({dev} and {t.device})")
+            dev = at
+        elif at != dev:
+            raise MsaError(f"tensors on different devices (cuda:{dev} and {t.device})")
 
 
 def _arg(name: str, t, dtype: torch.dtype, shape: Optional[Sequence[int]] = None,
@@ -277,6 +278,9 @@ def _arg(name: str, t, dtype: torch.dtype, shape: Optional[Sequence[int]] = None
     """Host check of one tensor argument against the layout the C entry point
     reads: dtype, exact shape (or element count for blocked layouts) and
     row-major contiguity.  Raises MsaError before anything reaches the device."""
+    if type(t) is torch.Tensor and numel is None and t.dtype is dtype and (shape is None or t.shape == shape) \
+            and t.is_contiguous():
+        return                                        # as asked: the rest names what is not
     if t is None:
         if optional:
             return
@@ -998,20 +1002,38 @@ def msa_version() -> str:
     return load_library().msa_version().decode()
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The device of a call's tensors made current, and its stream: yields the
-    stream's handle.  What is allocated inside belongs to that stream, so that
-    a workspace or output released after an unchecked call on a side stream is
-    not handed out while the call still runs."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-            return
-        if stream.device != device:
+class _on:
+    """The device of a call's tensors made current, and its stream: `with` gives
+    the stream's handle.  What is allocated inside belongs to that stream, so
+    that a workspace or output released after an unchecked call on a side stream
+    is not handed out while the call still runs.  With the current stream of the
+    current device, as most calls have it, nothing is switched: a switch costs
+    5 us of a call that may take ten."""
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
             raise MsaError(f"stream of {stream.device}, tensors on {device}")
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is None and self.device.index == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.device))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        self.stack.enter_context(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    """A tensor's address for an argument that is declared void *."""
+    return None if t is None else t.data_ptr()
 
 
 def _decay(decay: float) -> float:
@@ -1052,16 +1074,16 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
     _require_cuda(q, k_pages, v_pages, out, lse, weights, ws, *getattr(pages, "_keep", ()))
     with _on(q.device, stream) as handle:
         if out is None:
-            out = torch.empty((B, shape.H, shape.d), dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = torch.empty((B, shape.H), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, shape.H), dtype=torch.float32)
         if ws is None:
             need = msa_dense_attn_decode_paged_workspace_size(shape, pages, weights is not None)
             if need == 0:
                 raise MsaError("msa_dense_attn_decode_paged: shape or paged description rejected")
             ws = _workspace(need, q.device)
-        rc = lib.msa_dense_attn_decode_paged(ctypes.byref(shape), ctypes.byref(pages), _ptr(q), _ptr(k_pages),
-                                             _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(weights), decay, _ptr(ws),
+        rc = lib.msa_dense_attn_decode_paged(ctypes.byref(shape), ctypes.byref(pages), _at(q), _at(k_pages),
+                                             _at(v_pages), _at(out), _at(lse), _at(weights), decay, _at(ws),
                                              _nbytes(ws), handle)
         _check(rc, "msa_dense_attn_decode_paged")
         if check:
@@ -1102,8 +1124,8 @@ def msa_attn_weights(shape: Shape, seqs: Varlen, q: torch.Tensor, k: torch.Tenso
             if need == 0:
                 raise MsaError("msa_attn_weights: shape or sequence description rejected")
             ws = _workspace(need, q.device)
-        rc = lib.msa_attn_weights(ctypes.byref(shape), ctypes.byref(seqs), _ptr(q), _ptr(k), _ptr(lse), _ptr(weights),
-                                  int(weights.shape[2]), decay, _ptr(ws), _nbytes(ws), handle)
+        rc = lib.msa_attn_weights(ctypes.byref(shape), ctypes.byref(seqs), _at(q), _at(k), _at(lse), _at(weights),
+                                  int(weights.shape[2]), decay, _at(ws), _nbytes(ws), handle)
         _check(rc, "msa_attn_weights")
         if check:
             _device_check(ws, stream, "msa_attn_weights")
@@ -1138,16 +1160,16 @@ def msa_evict_select(shape: Shape, pages: Paged, weights: torch.Tensor, budget: 
     _require_cuda(weights, kept, new_lens, ws, *getattr(pages, "_keep", ()))
     with _on(weights.device, stream) as handle:
         if kept is None:
-            kept = torch.empty((B, R, budget), dtype=torch.int32, device=weights.device)
+            kept = weights.new_empty((B, R, budget), dtype=torch.int32)
         if new_lens is None:
-            new_lens = torch.empty((B,), dtype=torch.int32, device=weights.device)
+            new_lens = weights.new_empty((B,), dtype=torch.int32)
         if ws is None:
             need = msa_evict_select_workspace_size(shape, pages, per_group)
             if need == 0:
                 raise MsaError("msa_evict_select: shape or paged description rejected")
             ws = _workspace(need, weights.device)
-        rc = lib.msa_evict_select(ctypes.byref(shape), ctypes.byref(pages), _ptr(weights), budget, int(n_sink),
-                                  int(n_recent), 1 if per_group else 0, _ptr(kept), _ptr(new_lens), _ptr(ws),
+        rc = lib.msa_evict_select(ctypes.byref(shape), ctypes.byref(pages), _at(weights), budget, int(n_sink),
+                                  int(n_recent), 1 if per_group else 0, _at(kept), _at(new_lens), _at(ws),
                                   _nbytes(ws), handle)
         _check(rc, "msa_evict_select")
         if check:
@@ -1201,9 +1223,9 @@ def msa_evict_move(shape: Shape, pages: Paged, new_pages: Paged, kept: torch.Ten
             if need == 0:
                 raise MsaError("msa_evict_move: shape or paged description rejected")
             ws = _workspace(need, kept.device)
-        rc = lib.msa_evict_move(ctypes.byref(shape), ctypes.byref(pages), ctypes.byref(new_pages), _ptr(kept),
-                                int(kept.shape[2]), 1 if per_group else 0, _ptr(k_pages), _ptr(v_pages),
-                                _ptr(k_idx_pages), _ptr(weights), _ptr(weights_out), _ptr(ws), _nbytes(ws), handle)
+        rc = lib.msa_evict_move(ctypes.byref(shape), ctypes.byref(pages), ctypes.byref(new_pages), _at(kept),
+                                int(kept.shape[2]), 1 if per_group else 0, _at(k_pages), _at(v_pages),
+                                _at(k_idx_pages), _at(weights), _at(weights_out), _at(ws), _nbytes(ws), handle)
         _check(rc, "msa_evict_move")
         if check:
             _device_check(ws, stream, "msa_evict_move")
