@@ -49,17 +49,19 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 __host__ __device__ constexpr int stage_bytes() { return 2 * 64 * D * 2; }          // keys and values of one tile
+// 128 KB in flight per SM.  The loads alone, without the products: 1 x 1M tokens in 430 us with 64 KB, 306 us with
+// 128 KB and 342 us with 192 KB, where more requests meet in L2 than it takes in order.
 template <int D>
-__host__ __device__ constexpr int num_stages() { return D == 128 ? 6 : 10; }
+__host__ __device__ constexpr int num_stages() { return D == 128 ? 4 : 8; }
 // Half the output fragments of four warps: the sums are merged in two halves of the columns, which leaves the
 // join's first CTAs room beside this kernel's (they are in place when it ends).
 template <int D>
 __host__ __device__ constexpr int merge_bytes() { return 4 * 16 * (D / 2) * 4; }
 
 struct DecCtl {
-  uint64_t full[10];
-  uint64_t empty[10];
-  int32_t valid[10];            // tokens of the tile to attend (0: its page is outside the cache)
+  uint64_t full[8];
+  uint64_t empty[8];
+  int32_t valid[8];             // tokens of the tile to attend (0: its page is outside the cache)
   int32_t warp_sum[10];
   int32_t first_seq, first_start, total;
   int32_t lens[kDecThreads];    // the batch's lengths, where a thread has one at most
@@ -76,8 +78,9 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+// (Not volatile: a function of its registers, which the compiler may place among the loads.)
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -208,6 +211,7 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
   if (warp == kComputeWarps) {
     // ------------------------------------------------------------ loads
+    const uint64_t once = evict_first_policy();
     bool ok = true;
     int issued = 0;
     for (int t = lo; t < hi;) {
@@ -239,8 +243,8 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
               uint8_t* dst = smem + st * STAGE;
               const int row = page * kBk + (j0 & (kBk - 1));
               mbar_arrive_expect_tx(&ctl->full[st], STAGE);
-              tma_load_3d(dst, &tm_k, &ctl->full[st], 0, row, 0);
-              tma_load_3d(dst + KV, &tm_v, &ctl->full[st], 0, row, 0);
+              tma_load_3d_hint(dst, &tm_k, &ctl->full[st], 0, row, 0, once);
+              tma_load_3d_hint(dst + KV, &tm_v, &ctl->full[st], 0, row, 0, once);
             } else {
               report_error(err, MSA_ERR_DEVICE_CHECK, kSiteDenseDecode, b, blk);
               mbar_arrive(&ctl->full[st]);
@@ -312,18 +316,32 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const int valid = ctl->valid[st] - sub * kTileTok;      // tokens of this warp to attend
       float sc[2][4];                                          // scores: tokens 0-7 and 8-15 of the warp
       const uint32_t base = smem0 + st * STAGE + grp;
+      uint32_t f[KK][4];                                       // the keys' fragments, then the values'
       if (valid > 0) {
+        // every load ahead of the products, and two chains of products a half: a warp's time on a tile is
+        // latency, and it is what holds the stage
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+          ldsm_x4(base + (kk >> 2) * line + k_row + ((((kk & 3) * 2 + k_bit) ^ swz) << 4), f[kk]);
+        float odd[2][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sc[n][x] = 0.f;
+          for (int x = 0; x < 4; ++x) sc[n][x] = odd[n][x] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          uint32_t f[4];
-          ldsm_x4(base + (kk >> 2) * line + k_row + ((((kk & 3) * 2 + k_bit) ^ swz) << 4), f);
-          mma_16816(sc[0], qf[kk], f[0], f[1]);
-          mma_16816(sc[1], qf[kk], f[2], f[3]);
+        for (int kk = 0; kk < KK; kk += 2) {
+          mma_16816(sc[0], qf[kk], f[kk][0], f[kk][1]);
+          mma_16816(sc[1], qf[kk], f[kk][2], f[kk][3]);
+          mma_16816(odd[0], qf[kk + 1], f[kk + 1][0], f[kk + 1][1]);
+          mma_16816(odd[1], qf[kk + 1], f[kk + 1][2], f[kk + 1][3]);
         }
+#pragma unroll
+        for (int n2 = 0; n2 < KK / 2; ++n2)
+          ldsm_x4_trans(base + KV + (n2 >> 2) * line + v_row + ((((n2 & 3) * 2 + v_bit) ^ swz) << 4), f[n2]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[n][x] += odd[n][x];
         if (valid < kTileTok) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
@@ -378,24 +396,33 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ph[2 * n + y] = hi2;
             pl[2 * n + y] = pack_bf16x2(p0 - __uint_as_float(hi2 << 16), p1 - __uint_as_float(hi2 & 0xffff0000u));
           }
+#pragma unroll
+        for (int n2 = KK / 2; n2 < KK; ++n2)     // (all of them ahead of the softmax would not fit in the registers)
+          ldsm_x4_trans(base + KV + (n2 >> 2) * line + v_row + ((((n2 & 3) * 2 + v_bit) ^ swz) << 4), f[n2]);
         // value rows past the last token may hold anything (0 x inf is no 0): cleared in the operand
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (valid < kTileTok) {
           keep0 = (c2 < valid ? 0xffffu : 0u) | (c2 + 1 < valid ? 0xffff0000u : 0u);
           keep1 = (c2 + 8 < valid ? 0xffffu : 0u) | (c2 + 9 < valid ? 0xffff0000u : 0u);
         }
+        if (valid < kTileTok) {
+#pragma unroll
+          for (int n2 = 0; n2 < KK; ++n2) {
+            f[n2][0] &= keep0;
+            f[n2][1] &= keep1;
+            f[n2][2] &= keep0;
+            f[n2][3] &= keep1;
+          }
+        }
 #pragma unroll
         for (int n2 = 0; n2 < KK; ++n2) {
-          uint32_t f[4];
-          ldsm_x4_trans(base + KV + (n2 >> 2) * line + v_row + ((((n2 & 3) * 2 + v_bit) ^ swz) << 4), f);
-          f[0] &= keep0;
-          f[1] &= keep1;
-          f[2] &= keep0;
-          f[3] &= keep1;
-          mma_16816(o[2 * n2], ph, f[0], f[1]);
-          mma_16816(o[2 * n2 + 1], ph, f[2], f[3]);
-          mma_16816(o[2 * n2], pl, f[0], f[1]);
-          mma_16816(o[2 * n2 + 1], pl, f[2], f[3]);
+          mma_16816(o[2 * n2], ph, f[n2][0], f[n2][1]);
+          mma_16816(o[2 * n2 + 1], ph, f[n2][2], f[n2][3]);
+        }
+#pragma unroll
+        for (int n2 = 0; n2 < KK; ++n2) {
+          mma_16816(o[2 * n2], pl, f[n2][0], f[n2][1]);
+          mma_16816(o[2 * n2 + 1], pl, f[n2][2], f[n2][3]);
         }
       }
       __syncwarp();
@@ -722,7 +749,9 @@ int launch_split(const DenseDecodeArgs& a, int ctas, const CUtensorMap& tm_k, co
                  int logit_tiles, cudaStream_t st) {
   constexpr int smem = 1024 + num_stages<D>() * stage_bytes<D>() + merge_bytes<D>() + (int)sizeof(DecCtl);
   static_assert(smem <= 220 * 1024, "shared memory of one CTA, and 7 KB for the join's beside it");
-  static_assert(num_stages<D>() <= 10, "barriers of the stages");
+  static_assert(num_stages<D>() <= 8, "barriers of the stages");
+  // a stage belongs to one set: a set that saw every other phase of it could not tell them by parity
+  static_assert(num_stages<D>() % kSets == 0, "stages per set");
   static std::atomic<uint64_t> ready{0};
   const int rc = allow_smem(dense_decode_kernel<D, kWeights>, smem, &ready);
   if (rc != 0) return rc;
