@@ -39,6 +39,22 @@ int allow_smem(K* kernel, int bytes, std::atomic<uint64_t>* done) {
   return (int)e;
 }
 
+// A launch whose grid may start before the one ahead of it in the stream has
+// ended (it waits for that with griddepcontrol.wait).
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 struct DenseDecodeArgs {
   const void* q;              // bf16 [batch, H, d]
   const void* k_pages;        // bf16 [num_pages * 128, G, d]
@@ -95,11 +111,11 @@ struct EvictSelectArgs {
   int32_t batch, G, per_group, max_seqlen, budget, n_sink, n_recent;
   int32_t* kept;              // [batch, per_group ? G : 1, budget]
   int32_t* new_lens;          // [batch]
-  uint32_t* keys;             // evict_select_keys_bytes of workspace
-  DevError* err;
+  void* work;                 // evict_select_work_bytes of workspace, right behind the header of err
+  DevError* err;              // cleared by the launcher
 };
-// Workspace for the ranking keys (0 where they fit in shared memory).
-size_t evict_select_keys_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen);
+// Workspace behind the header (0 where a sequence's keys fit in a cluster's shared memory).
+size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen);
 int launch_evict_select(const EvictSelectArgs& a, void* stream);
 
 struct EvictMoveArgs {

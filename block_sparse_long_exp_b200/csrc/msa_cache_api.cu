@@ -92,7 +92,7 @@ msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs
 
 size_t msa_evict_select_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages, int32_t per_group) {
   if (check_paged(shape, pages) != MSA_OK) return 0;
-  return kWsHeader + evict_select_keys_bytes(pages->batch, per_group != 0 ? shape->G : 1, pages->max_seqlen);
+  return kWsHeader + evict_select_work_bytes(pages->batch, per_group != 0 ? shape->G : 1, pages->max_seqlen);
 }
 
 msa_status_t msa_evict_select(const msa_shape_t* shape, const msa_paged_t* pages, const float* weights,
@@ -104,13 +104,12 @@ msa_status_t msa_evict_select(const msa_shape_t* shape, const msa_paged_t* pages
   if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget) return MSA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, msa_evict_select_workspace_size(shape, pages, per_group))) return MSA_ERR_WORKSPACE;
   if ((int64_t)pages->batch * shape->G * 8 > INT32_MAX) return MSA_ERR_UNSUPPORTED;      // CTAs of one launch
-  if (!clear_error(ws, stream)) return MSA_ERR_CUDA;
   EvictSelectArgs a{};
   a.weights = weights; a.width = (int64_t)pages->max_blocks * kBk; a.seqlens = pages->seqlens;
   a.batch = pages->batch; a.G = shape->G; a.per_group = per_group != 0; a.max_seqlen = pages->max_seqlen;
   a.budget = budget; a.n_sink = n_sink; a.n_recent = n_recent;
   a.kept = kept; a.new_lens = new_lens;
-  a.keys = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  a.work = static_cast<uint8_t*>(ws) + kWsHeader;
   a.err = static_cast<DevError*>(ws);
   return launch_evict_select(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
 }

@@ -763,22 +763,6 @@ int launch_split(const DenseDecodeArgs& a, int ctas, const CUtensorMap& tm_k, co
   return (int)cudaGetLastError();
 }
 
-// A launch whose grid may start before the one ahead of it in the stream has
-// ended (it waits for that with griddepcontrol.wait).
-template <typename... P, typename... A>
-int launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
 int logit_tiles_of(int32_t max_seqlen) { return (max_seqlen + 63) / 64 * 4; }   // whole tiles of every G
 
 }  // namespace

@@ -20,6 +20,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "msa_common.cuh"
 #include "msa_cache.h"
 #include "msa_gather.h"
@@ -34,17 +36,10 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelTile = kSelThreads * 4;        // tokens per step of a CTA
-constexpr int kKeysInSmem = 40960;               // keys a CTA keeps in shared memory (160 KB)
-constexpr int kMaxCluster = 8;
+constexpr int kSelPer = 8;                       // tokens of a thread, in its registers
+constexpr int kSelPart = kSelThreads * kSelPer;  // tokens of a CTA
+constexpr int kMaxCluster = 4;
 constexpr uint32_t kForced = 0xffffffffu;        // above +inf's key
-
-struct SelCtl {
-  uint32_t hist[3][2048];
-  uint32_t warp_sum[kSelWarps];
-  uint32_t bin, above;        // the bin the budget ends in, keys above it
-  uint32_t gt, eq;            // this CTA's keys above and equal to the threshold
-};
 
 // 32-bit key in the order of the scores; NaN lowest, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(uint32_t u) {
@@ -63,8 +58,64 @@ __device__ __forceinline__ float narrow(double x) {
   asm("cvt.rn.f32.f64 %0, %1;" : "=f"(y) : "d"(x));
   return y;
 }
+// A finite f32 times 2^-896 as an f64: sign, exponent field and fraction moved
+// to their places (0 and denormals too: the fields mean the same one scale
+// down).  A conversion instruction would run at an eighth of the rate.
+__device__ __forceinline__ double scaled_down(uint32_t u) {
+  return __hiloint2double((int)((u & 0x80000000u) | ((u & 0x7fffffffu) >> 3)), (int)(u << 29));
+}
+// Its way back, rounded to nearest even: the f32's bits.  A sum in between is
+// the f64 sum times 2^-896: multiples of 2^-149 keep all their bits there.
+__device__ __forceinline__ uint32_t scaled_up(double s) {
+  const uint32_t hi = (uint32_t)__double2hiint(s), lo = (uint32_t)__double2loint(s);
+  uint32_t u = ((hi & 0x7fffffffu) << 3) | (lo >> 29);
+  const uint32_t rest = lo & 0x1fffffffu;
+  u += (rest > 0x10000000u || (rest == 0x10000000u && (u & 1u))) ? 1u : 0u;
+  return (hi & 0x80000000u) | min(u, 0x7f800000u);
+}
 
-// Exclusive sum over the block in thread order (all threads call; two barriers).
+// Scores (as bits) of N tokens in a row: the sum over GS groups' weights in 64
+// bits, rounded once to 32.
+template <int GS, int N>
+__device__ __forceinline__ void token_scores(const float* __restrict__ w, int64_t width, uint32_t (&u)[N]) {
+  uint4 v[GS][N / 4];
+#pragma unroll
+  for (int g = 0; g < GS; ++g)
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) v[g][q] = *reinterpret_cast<const uint4*>(w + g * width + 4 * q);
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t c[GS];
+#pragma unroll
+      for (int g = 0; g < GS; ++g) c[g] = x == 0 ? v[g][q].x : x == 1 ? v[g][q].y : x == 2 ? v[g][q].z : v[g][q].w;
+      if constexpr (GS == 1) {
+        u[4 * q + x] = c[0];
+      } else {
+        bool finite = true;
+        double s = 0.0;
+#pragma unroll
+        for (int g = 0; g < GS; ++g) {
+          finite &= (c[g] & 0x7f800000u) != 0x7f800000u;
+          s = g == 0 ? scaled_down(c[0]) : s + scaled_down(c[g]);
+        }
+        u[4 * q + x] = scaled_up(s);
+        if (!finite) {
+          double t = widen(__uint_as_float(c[0]));
+#pragma unroll
+          for (int g = 1; g < GS; ++g) t += widen(__uint_as_float(c[g]));
+          u[4 * q + x] = __float_as_uint(narrow(t));
+        }
+      }
+    }
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Exclusive sum over the block of WARPS warps in thread order (all threads call; two barriers).
+template <int WARPS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t incl = v;
@@ -76,7 +127,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   __syncthreads();                               // the sums of the scan before are read
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  uint32_t w = warp_sum[lane];
+  uint32_t w = lane < WARPS ? warp_sum[lane] : 0u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(0xffffffffu, w, o);
@@ -87,156 +138,391 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   return incl - v + (warp == 0 ? 0u : before);
 }
 
+// Counts a bin (whole warps call).  A warp of one bin (weights that are all zero) adds once.
+__device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in) {
+  const uint32_t m = __ballot_sync(0xffffffffu, in);
+  if (m == 0) return;
+  const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
+  if (__all_sync(0xffffffffu, !in || bin == first)) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(&hist[first], __popc(m));
+  } else if (in) {
+    atomicAdd(&hist[bin], 1u);
+  }
+}
+
+// Of 32 counts, a lane each, the lane in which the `need` first ones end, from the top; *above: those before it.
+__device__ __forceinline__ int find_lane(uint32_t c, uint32_t need, uint32_t* above) {
+  const int lane = threadIdx.x & 31;
+  uint32_t incl = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_down_sync(0xffffffffu, incl, o);
+    if (lane + o < 32) incl += x;
+  }
+  const int at = __ffs(__ballot_sync(0xffffffffu, incl - c < need && need <= incl)) - 1;
+  *above = __shfl_sync(0xffffffffu, incl - c, at);
+  return at;
+}
+
+struct SelCtl {
+  uint32_t hist[3][2048];
+  uint32_t sum[2048];         // a cluster's histogram
+  uint32_t warp_sum[kSelWarps];
+  uint32_t gt, eq;            // this CTA's keys above and equal to the threshold
+};
+
+template <bool kCluster, int GS>
 __global__ void __launch_bounds__(kSelThreads, 1)
-evict_select_kernel(const float* __restrict__ weights, int G, int per_group, int64_t width,
-                    const int32_t* __restrict__ seqlens, int max_seqlen, int budget, int n_sink, int n_recent,
-                    int32_t* __restrict__ kept, int32_t* __restrict__ new_lens, uint32_t* __restrict__ ws_keys,
-                    int64_t ws_stride, DevError* err) {
-  extern __shared__ uint8_t smem_raw[];
-  SelCtl* ctl = reinterpret_cast<SelCtl*>(smem_raw);
-  uint32_t* smem_keys = reinterpret_cast<uint32_t*>(smem_raw + sizeof(SelCtl));
+evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, const int32_t* __restrict__ seqlens,
+                    int batch, int max_seqlen, int budget, int n_sink, int n_recent, int32_t* __restrict__ kept,
+                    int32_t* __restrict__ new_lens, DevError* err) {
+  __shared__ SelCtl ctl;
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = cluster.num_blocks(), rank = cluster.block_rank();
-  const int R = per_group ? G : 1;
+  const int cs = kCluster ? cluster.num_blocks() : 1, rank = kCluster ? cluster.block_rank() : 0;
+  const int R = GS == 1 ? G : 1;
   const int row = blockIdx.x / cs;                // (sequence, ranking)
   const int b = row / R, r = row - b * R;
-  const int tid = threadIdx.x;
-  const int raw_len = seqlens[b];
-  const int L = (raw_len < 0 || raw_len > max_seqlen) ? 0 : raw_len;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bounded = [&](int n) { return n < 0 || n > max_seqlen ? 0 : n; };
+  const int L = bounded(seqlens[b]);
   int32_t* dst = kept + (int64_t)row * budget;
-  if (rank == 0 && tid == 0) {
-    if (r == 0) new_lens[b] = L < budget ? L : budget;
-    if (L != raw_len) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, b, raw_len);
+  if (rank == 0 && tid == 0 && r == 0) new_lens[b] = L < budget ? L : budget;
+  if (blockIdx.x == 0) {                          // the first bad length, or none
+    int bad = batch;
+    for (int i = tid; i < batch; i += kSelThreads)
+      if (bounded(seqlens[i]) != seqlens[i]) bad = min(bad, i);
+    bad = __reduce_min_sync(0xffffffffu, bad);
+    if (lane == 0) ctl.warp_sum[warp] = bad;
+    __syncthreads();
+    if (warp == 0) {
+      bad = __reduce_min_sync(0xffffffffu, (int)ctl.warp_sum[lane]);
+      if (lane == 0)
+        *err = bad < batch ? DevError{MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, bad, seqlens[bad]} : DevError{0, 0, 0, 0};
+    }
+    __syncthreads();
   }
   if (L <= budget) {                              // every token stays (the whole cluster takes this way)
     for (int64_t i = rank * kSelThreads + tid; i < budget; i += cs * kSelThreads) dst[i] = i < L ? (int32_t)i : -1;
     return;
   }
 
-  for (int i = tid; i < 3 * 2048; i += kSelThreads) (&ctl->hist[0][0])[i] = 0u;
+  // ---- this CTA's tokens [j0, j0 + n), eight in a row to a thread
+  const int per = (L + cs - 1) / cs + (kSelPer - 1) & ~(kSelPer - 1);
+  const int j0 = min(rank * per, L), n = min(per, L - j0);
+  const int i0 = tid * kSelPer;
+  uint32_t key[kSelPer];
+#pragma unroll
+  for (int x = 0; x < kSelPer; ++x) key[x] = 0u;
+  if (i0 < n) token_scores<GS>(weights + ((int64_t)b * G + r) * width + j0 + i0, width, key);   // rows reach past L to their width
+  for (int i = tid; i < 3 * 2048; i += kSelThreads) (&ctl.hist[0][0])[i] = 0u;
   __syncthreads();
-
-  // this CTA's tokens [j0, j1)
-  const int per = ((L + cs - 1) / cs + 3) / 4 * 4;
-  const int j0 = min(rank * per, L), j1 = min(j0 + per, L);
-  const int n = j1 - j0;
-  uint32_t* keys = n <= kKeysInSmem ? smem_keys : ws_keys + (int64_t)row * ws_stride + j0;
-
-  // ---- keys, and the histogram of their top 11 bits
-  const float* w0 = weights + ((int64_t)b * G + r) * width + j0;   // 16-byte aligned: width % 128 == 0, j0 % 4 == 0
-  for (int i = tid * 4; i < n; i += kSelTile) {
-    uint32_t u[4];
-    if (R == G) {
-      const float4 v = *reinterpret_cast<const float4*>(w0 + i);   // the row reaches past L to its width
-      u[0] = __float_as_uint(v.x); u[1] = __float_as_uint(v.y); u[2] = __float_as_uint(v.z); u[3] = __float_as_uint(v.w);
-    } else {
-      double s[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-      for (int g = 0; g < G; ++g) {
-        const float4 v = *reinterpret_cast<const float4*>(w0 + (int64_t)g * width + i);
-        s[0] += widen(v.x); s[1] += widen(v.y); s[2] += widen(v.z); s[3] += widen(v.w);
-      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) u[x] = __float_as_uint(narrow(s[x]));
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int j = j0 + i + x;
-      const uint32_t key = (j < n_sink || j >= L - n_recent) ? kForced : order_key(u[x]);
-      if (i + x < n) {
-        keys[i + x] = key;
-        atomicAdd(&ctl->hist[0][key >> 21], 1u);
-      }
-    }
+  for (int x = 0; x < kSelPer; ++x) {
+    const int j = j0 + i0 + x;
+    key[x] = (j < n_sink || j >= L - n_recent) ? kForced : order_key(key[x]);
   }
 
-  // ---- the threshold, 11 + 11 + 10 bits
-  uint32_t need = budget, top = 0;                // keys still to take; the bits found so far
-#pragma unroll 1
+  // ---- the threshold, 11 + 11 + 10 bits: keys still to take, and the bits found so far
+  uint32_t need = budget, top = 0;
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int nbin = pass == 2 ? 1024 : 2048;
-    if (pass > 0) {
-      const int shift = pass == 1 ? 21 : 10, down = pass == 1 ? 10 : 0;
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = keys[i];
-        if ((key >> shift) == top) atomicAdd(&ctl->hist[pass][(key >> down) & (nbin - 1)], 1u);
-      }
-    }
-    cluster.sync();
-    // bins from the top: thread t has 2 t and 2 t + 1 from there
-    uint32_t c0 = 0, c1 = 0;
-    const int b0 = nbin - 1 - 2 * tid;
-    if (b0 > 0) {
+    constexpr int kShift[3] = {0, 21, 10}, kDown[3] = {21, 10, 0};
+    uint32_t* hist = ctl.hist[pass];
+#pragma unroll
+    for (int x = 0; x < kSelPer; ++x)
+      count_bin(hist, key[x] >> kDown[pass] & (pass == 2 ? 1023u : 2047u),
+                i0 + x < n && (pass == 0 || key[x] >> kShift[pass] == top));
+    // a thread has two bins; every warp finds the bin from the warps' sums
+    uint2 c = make_uint2(0u, 0u);
+    if constexpr (kCluster) {
+      cluster.sync();
       for (int k = 0; k < cs; ++k) {
-        const uint32_t* h = cluster.map_shared_rank(&ctl->hist[pass][0], k);
-        const uint2 v = *reinterpret_cast<const uint2*>(h + b0 - 1);
-        c0 += v.y;
-        c1 += v.x;
+        const uint2 v = reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, k))[tid];
+        c.x += v.x;
+        c.y += v.y;
       }
+      reinterpret_cast<uint2*>(ctl.sum)[tid] = c;
+      hist = ctl.sum;
+    } else {
+      __syncthreads();
+      c = reinterpret_cast<const uint2*>(hist)[tid];
     }
-    uint32_t total;
-    const uint32_t before = block_scan(c0 + c1, ctl->warp_sum, &total);
-    if (before < need && need <= before + c0 + c1) {
-      const bool first = need <= before + c0;
-      ctl->bin = first ? b0 : b0 - 1;
-      ctl->above = first ? before : before + c0;
-    }
+    const uint32_t w = __reduce_add_sync(0xffffffffu, c.x + c.y);
+    if (lane == 0) ctl.warp_sum[warp] = w;
     __syncthreads();
-    top = pass == 2 ? (top << 10 | ctl->bin) : (top << 11 | ctl->bin);
-    need -= ctl->above;
+    uint32_t above, more;
+    const int at = find_lane(ctl.warp_sum[lane], need, &above);
+    const uint2 d = reinterpret_cast<const uint2*>(hist)[32 * at + lane];
+    const int bl = find_lane(d.x + d.y, need - above, &more);
+    const uint32_t upper = __shfl_sync(0xffffffffu, d.y, bl);
+    need -= above + more;
+    const bool high = need <= upper;              // the upper of the lane's two bins
+    if (!high) need -= upper;
+    const uint32_t bin = 64 * at + 2 * bl + (high ? 1 : 0);
+    top = top << (pass == 2 ? 10 : 11) | bin;
   }
   // keys above `top` all stay, and the first `need` of those equal to it
 
-  // ---- how many of this CTA's keys are above and equal
-  uint32_t mine = 0;
-  {
-    const uint32_t d[3] = {top >> 21, (top >> 10) & 2047u, top & 1023u};
-    for (int pass = 0; pass < 3; ++pass)
-      for (int i = tid; i < (pass == 2 ? 1024 : 2048); i += kSelThreads)
-        if ((uint32_t)i > d[pass]) mine += ctl->hist[pass][i];
-    uint32_t total;
-    block_scan(mine, ctl->warp_sum, &total);
+  uint32_t f = 0;                                 // above | equal << 16 of the thread's eight
+#pragma unroll
+  for (int x = 0; x < kSelPer; ++x)
+    if (i0 + x < n) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
+  uint32_t total;
+  const uint32_t before = block_scan<kSelWarps>(f, ctl.warp_sum, &total);
+  uint32_t gt = before & 0xffffu, eq = before >> 16;
+  if constexpr (kCluster) {                       // and of the CTAs before this one
     if (tid == 0) {
-      ctl->gt = total;
-      ctl->eq = ctl->hist[2][d[2]];
+      ctl.gt = total & 0xffffu;
+      ctl.eq = total >> 16;
+    }
+    cluster.sync();
+    for (int k = 0; k < rank; ++k) {
+      const SelCtl* other = cluster.map_shared_rank(&ctl, k);
+      gt += other->gt;
+      eq += other->eq;
     }
   }
-  cluster.sync();
-  uint32_t gt = 0, eq = 0;                        // of the CTAs before this one
-  for (int k = 0; k < rank; ++k) {
-    const SelCtl* other = cluster.map_shared_rank(ctl, k);
-    gt += other->gt;
-    eq += other->eq;
+#pragma unroll
+  for (int x = 0; x < kSelPer; ++x) {
+    if (i0 + x >= n) break;
+    if (key[x] > top) {
+      dst[gt + min(eq, need)] = j0 + i0 + x;
+      ++gt;
+    } else if (key[x] == top) {
+      if (eq < need) dst[gt + eq] = j0 + i0 + x;
+      ++eq;
+    }
   }
+  if constexpr (kCluster) cluster.sync();         // the others read this CTA's counts
+}
 
-  // ---- the kept tokens in order
-  for (int base = 0; base < n; base += kSelTile) {
-    const int i = base + tid * 4;
-    uint32_t f = 0;                               // above | equal << 16 of the thread's four
-    uint32_t key[4];
+// -------------------------------------------------- select, long sequences ---
+//
+// The same search with a CTA per 8192 tokens of every (sequence, ranking), the
+// histograms in global memory and a launch per step: the keys and the histogram
+// of their top 11 bits; of the next 11; of the last 10; each part's numbers of
+// kept tokens; the kept tokens.  Every CTA finds the step's bin by itself.
+
+constexpr int kLongThreads = 512;
+constexpr int kLongPart = 8192;                   // tokens per CTA
+constexpr int kLongPer = kLongPart / kLongThreads;
+
+struct LongRow {
+  uint32_t top, need;         // the bits found so far; keys still to take among those that share them
+};
+struct LongArgs {
+  const float* weights;
+  int64_t width;
+  const int32_t* seqlens;
+  int32_t G, R, parts, max_seqlen, budget, n_sink, n_recent;
+  int32_t* kept;
+  int32_t* new_lens;
+  uint32_t* keys;             // [rows, parts * 8192]
+  uint32_t* hist;             // [3, rows, 2048], zeroed
+  LongRow* found;             // [3, rows]
+  uint2* counts;              // [rows, parts]: keys above and equal to the threshold
+  int32_t rows;
+  DevError* err;
+};
+
+// The bin in which the `need` largest keys of a histogram end, and the keys above it (all threads call).
+template <int BINS>
+__device__ __forceinline__ void find_bin(const uint32_t* __restrict__ hist, uint32_t need, uint32_t* warp_sum,
+                                         uint32_t* out, uint32_t* bin, uint32_t* above) {
+  constexpr int N = BINS / kLongThreads;          // thread t has the bins N t .. N t + N - 1 from the top
+  uint32_t c[N], sum = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      key[x] = i + x < n ? keys[i + x] : 0u;
-      if (i + x < n) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
+  for (int i = 0; i < N; ++i) {
+    c[i] = hist[BINS - 1 - (N * (int)threadIdx.x + i)];
+    sum += c[i];
+  }
+  uint32_t total;
+  uint32_t before = block_scan<kLongThreads / 32>(sum, warp_sum, &total);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (before < need && need <= before + c[i]) {
+      out[0] = BINS - 1 - (N * threadIdx.x + i);
+      out[1] = before;
     }
-    uint32_t total;
-    const uint32_t before = block_scan(f, ctl->warp_sum, &total);
-    uint32_t g0 = gt + (before & 0xffffu), e0 = eq + (before >> 16);
+    before += c[i];
+  }
+  __syncthreads();
+  *bin = out[0];
+  *above = out[1];
+}
+
+// What the CTAs of every step share: their row and part of it.
+struct LongPlace {
+  int row, part, b, r, L, n;                      // n: tokens of the part
+  bool cut;                                       // the sequence is longer than the budget
+  __device__ LongPlace(const LongArgs& a) {
+    row = blockIdx.x / a.parts;
+    part = blockIdx.x - row * a.parts;
+    b = row / a.R;
+    r = row - b * a.R;
+    const int raw = a.seqlens[b];
+    L = (raw < 0 || raw > a.max_seqlen) ? 0 : raw;
+    cut = L > a.budget;
+    n = min(max(L - part * kLongPart, 0), kLongPart);
+  }
+};
+
+template <int GS>
+__global__ void __launch_bounds__(kLongThreads) long_keys_kernel(const LongArgs a) {
+  __shared__ uint32_t hist[2048];
+  pdl_launch_dependents();
+  const LongPlace p(a);
+  const int tid = threadIdx.x;
+  if (p.part == 0 && p.r == 0 && tid == 0) {
+    a.new_lens[p.b] = p.L < a.budget ? p.L : a.budget;
+    if (p.L != a.seqlens[p.b]) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, p.b, a.seqlens[p.b]);
+  }
+  if (!p.cut) {                                   // every token stays
+    int32_t* dst = a.kept + (int64_t)p.row * a.budget;
+    for (int64_t i = p.part * kLongThreads + tid; i < a.budget; i += (int64_t)a.parts * kLongThreads)
+      dst[i] = i < p.L ? (int32_t)i : -1;
+    return;
+  }
+  if (p.n == 0) return;
+  for (int i = tid; i < 2048; i += kLongThreads) hist[i] = 0u;
+  __syncthreads();
+  const int j0 = p.part * kLongPart;
+  const float* w0 = a.weights + ((int64_t)p.b * a.G + p.r) * a.width + j0;
+  uint32_t* keys = a.keys + (int64_t)blockIdx.x * kLongPart;
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) {
+    const int i = (s * kLongThreads + tid) * 4;
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
+    if (i < p.n) token_scores<GS>(w0 + i, a.width, u);               // the row reaches past L to its width
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      if (i + x >= n) break;
-      if (key[x] > top) {
-        dst[g0 + min(e0, need)] = j0 + i + x;
-        ++g0;
-      } else if (key[x] == top) {
-        if (e0 < need) dst[g0 + e0] = j0 + i + x;
-        ++e0;
+      const int j = j0 + i + x;
+      u[x] = (j < a.n_sink || j >= p.L - a.n_recent) ? kForced : order_key(u[x]);
+      count_bin(hist, u[x] >> 21, i + x < p.n);
+    }
+    *reinterpret_cast<uint4*>(keys + i) = make_uint4(u[0], u[1], u[2], u[3]);   // past the part's end: not counted
+  }
+  __syncthreads();
+  uint32_t* sum = a.hist + (int64_t)p.row * 2048;
+  for (int i = tid; i < 2048; i += kLongThreads)
+    if (hist[i] != 0) atomicAdd(&sum[i], hist[i]);
+}
+
+template <int PASS>
+__global__ void __launch_bounds__(kLongThreads) long_hist_kernel(const LongArgs a) {
+  constexpr int kBins = PASS == 2 ? 1024 : 2048;
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t warp_sum[kLongThreads / 32], out[2];
+  pdl_launch_dependents();
+  const LongPlace p(a);
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kBins; i += kLongThreads) hist[i] = 0u;
+  pdl_wait();                                     // every CTA: this grid's end stands for the ends before it
+  if (!p.cut || p.n == 0) return;
+  uint4 k[kLongPer / 4];
+  const uint4* keys = reinterpret_cast<const uint4*>(a.keys + (int64_t)blockIdx.x * kLongPart);
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) k[s] = keys[s * kLongThreads + tid];
+  LongRow f = PASS == 1 ? LongRow{0u, (uint32_t)a.budget} : a.found[(int64_t)a.rows + p.row];
+  uint32_t bin, above;
+  find_bin<2048>(a.hist + ((int64_t)(PASS - 1) * a.rows + p.row) * 2048, f.need, warp_sum, out, &bin, &above);
+  f.top = f.top << 11 | bin;
+  f.need -= above;
+  if (p.part == 0 && tid == 0) a.found[(int64_t)PASS * a.rows + p.row] = f;
+  constexpr int kShift = PASS == 1 ? 21 : 10, kDown = PASS == 1 ? 10 : 0;
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) {
+    const int i = (s * kLongThreads + tid) * 4;
+    const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      count_bin(hist, (u[x] >> kDown) & (kBins - 1), i + x < p.n && (u[x] >> kShift) == f.top);
+  }
+  __syncthreads();
+  uint32_t* sum = a.hist + ((int64_t)PASS * a.rows + p.row) * 2048;
+  for (int i = tid; i < kBins; i += kLongThreads)
+    if (hist[i] != 0) atomicAdd(&sum[i], hist[i]);
+}
+
+__global__ void __launch_bounds__(kLongThreads) long_count_kernel(const LongArgs a) {
+  __shared__ uint32_t warp_sum[kLongThreads / 32], out[2];
+  pdl_launch_dependents();
+  const LongPlace p(a);
+  const int tid = threadIdx.x;
+  pdl_wait();
+  if (!p.cut || p.n == 0) return;
+  uint4 k[kLongPer / 4];
+  const uint4* keys = reinterpret_cast<const uint4*>(a.keys + (int64_t)blockIdx.x * kLongPart);
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) k[s] = keys[s * kLongThreads + tid];
+  LongRow f = a.found[2ll * a.rows + p.row];
+  uint32_t bin, above;
+  find_bin<1024>(a.hist + (2ll * a.rows + p.row) * 2048, f.need, warp_sum, out, &bin, &above);
+  f.top = f.top << 10 | bin;
+  f.need -= above;
+  if (p.part == 0 && tid == 0) a.found[p.row] = f;
+  uint32_t c = 0;                                 // above | equal << 16
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) {
+    const int i = (s * kLongThreads + tid) * 4;
+    const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x < p.n) c += u[x] > f.top ? 1u : (u[x] == f.top ? 0x10000u : 0u);
+  }
+  uint32_t total;
+  block_scan<kLongThreads / 32>(c, warp_sum, &total);
+  if (tid == 0) a.counts[blockIdx.x] = make_uint2(total & 0xffffu, total >> 16);
+}
+
+__global__ void __launch_bounds__(kLongThreads) long_write_kernel(const LongArgs a) {
+  __shared__ uint32_t warp_sum[kLongThreads / 32];
+  const LongPlace p(a);
+  const int tid = threadIdx.x;
+  pdl_wait();
+  if (!p.cut || p.n == 0) return;
+  uint4 k[kLongPer / 4];                          // 16 tokens in a row
+  const uint4* keys = reinterpret_cast<const uint4*>(a.keys + (int64_t)blockIdx.x * kLongPart + tid * kLongPer);
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) k[s] = keys[s];
+  const LongRow f = a.found[p.row];
+  uint32_t g = 0, e = 0;                          // of the parts before this one
+  for (int i = tid; i < p.part; i += kLongThreads) {
+    const uint2 c = a.counts[(int64_t)p.row * a.parts + i];
+    g += c.x;
+    e += c.y;
+  }
+  uint32_t gt, eq, total;
+  block_scan<kLongThreads / 32>(g, warp_sum, &gt);
+  block_scan<kLongThreads / 32>(e, warp_sum, &eq);
+  uint32_t c = 0;
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) {
+    const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (tid * kLongPer + 4 * s + x < p.n) c += u[x] > f.top ? 1u : (u[x] == f.top ? 0x10000u : 0u);
+  }
+  const uint32_t before = block_scan<kLongThreads / 32>(c, warp_sum, &total);
+  gt += before & 0xffffu;
+  eq += before >> 16;
+  int32_t* dst = a.kept + (int64_t)p.row * a.budget;
+  const int j0 = p.part * kLongPart + tid * kLongPer;
+#pragma unroll
+  for (int s = 0; s < kLongPer / 4; ++s) {
+    const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (tid * kLongPer + 4 * s + x >= p.n) break;
+      if (u[x] > f.top) {
+        dst[gt + min(eq, f.need)] = j0 + 4 * s + x;
+        ++gt;
+      } else if (u[x] == f.top) {
+        if (eq < f.need) dst[gt + eq] = j0 + 4 * s + x;
+        ++eq;
       }
     }
-    gt += total & 0xffffu;
-    eq += total >> 16;
   }
-  cluster.sync();                                 // the others read this CTA's counts
 }
 
 // ------------------------------------------------------------------- move ---
@@ -265,7 +551,7 @@ __device__ __forceinline__ int bounded_len(int L, int most) { return (L < 0 || L
 // Marks every page of the sources and counts every page of the destinations,
 // so that the move can tell a page that is both, or twice a destination.
 __global__ void __launch_bounds__(256) evict_mark_kernel(const MoveArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the move waits for this grid's end
+  pdl_launch_dependents();                        // the move waits for this grid's end
   const int64_t src = (int64_t)a.batch * a.src_blocks, dst = (int64_t)a.batch * a.dst_blocks;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < src + dst; i += gridDim.x * 256ll) {
     const bool from = i < src;
@@ -285,7 +571,7 @@ __global__ void __launch_bounds__(256) evict_mark_kernel(const MoveArgs a) {
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a, int chunks) {
   __shared__ int64_t src_row[4][kMoveRows];       // row of the pages; -1: nothing to copy
   __shared__ int32_t from[4][kMoveRows];          // position in the source; -1: none
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   const int b = blockIdx.x / chunks, i0 = (blockIdx.x - b * chunks) * kMoveRows;
   const int tid = threadIdx.x;
   const int raw_src = a.src_lens[b], raw_dst = a.dst_lens[b];
@@ -367,34 +653,84 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   }
 }
 
-// CTAs per (sequence, ranking): one for every 8192 tokens, up to 8.
+// CTAs per (sequence, ranking).
 int cluster_of(int32_t max_seqlen) {
   int cs = 1;
-  while (cs < kMaxCluster && max_seqlen > cs * 8192) cs *= 2;
+  while (cs < kMaxCluster && max_seqlen > cs * kSelPart) cs *= 2;
   return cs;
+}
+
+// From here on a (sequence, ranking) has a CTA per 8192 tokens and five launches: LONGNOTE
+constexpr int32_t kLongFrom = kMaxCluster * kSelPart;
+
+struct LongLayout {
+  int32_t parts;
+  size_t keys, hist, found, counts, total;        // offsets after the header
+};
+LongLayout long_layout(int64_t rows, int32_t max_seqlen) {
+  LongLayout L{};
+  L.parts = (max_seqlen + kLongPart - 1) / kLongPart;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  L.hist = take(sizeof(uint32_t) * 3 * rows * 2048);       // first: cleared with the header
+  L.found = take(sizeof(LongRow) * 3 * rows);
+  L.counts = take(sizeof(uint2) * rows * L.parts);
+  L.keys = take(sizeof(uint32_t) * rows * L.parts * (size_t)kLongPart);
+  L.total = off;
+  return L;
+}
+
+int launch_long_select(const EvictSelectArgs& s, cudaStream_t st) {
+  const int R = s.per_group ? s.G : 1;
+  const int64_t rows = (int64_t)s.batch * R;
+  const LongLayout L = long_layout(rows, s.max_seqlen);
+  uint8_t* base = reinterpret_cast<uint8_t*>(s.work);
+  cudaError_t e = cudaMemsetAsync(s.err, 0, kWsHeader + sizeof(uint32_t) * 3 * rows * 2048, st);
+  if (e != cudaSuccess) return (int)e;
+  LongArgs a{};
+  a.weights = s.weights; a.width = s.width; a.seqlens = s.seqlens;
+  a.G = s.G; a.R = R; a.parts = L.parts; a.max_seqlen = s.max_seqlen; a.budget = s.budget;
+  a.n_sink = s.n_sink; a.n_recent = s.n_recent; a.kept = s.kept; a.new_lens = s.new_lens;
+  a.keys = reinterpret_cast<uint32_t*>(base + L.keys);
+  a.hist = reinterpret_cast<uint32_t*>(base + L.hist);
+  a.found = reinterpret_cast<LongRow*>(base + L.found);
+  a.counts = reinterpret_cast<uint2*>(base + L.counts);
+  a.rows = (int32_t)rows; a.err = s.err;
+  const dim3 grid((unsigned)(rows * L.parts));
+  {
+    ProfScope p("evict_select", st);
+    if (R == s.G) long_keys_kernel<1><<<grid, kLongThreads, 0, st>>>(a);
+    else if (s.G == 2) long_keys_kernel<2><<<grid, kLongThreads, 0, st>>>(a);
+    else long_keys_kernel<4><<<grid, kLongThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return (int)e;
+  }
+  prof_count_launch(4);
+  int rc = launch_after(long_hist_kernel<1>, grid, kLongThreads, st, a);
+  if (rc == 0) rc = launch_after(long_hist_kernel<2>, grid, kLongThreads, st, a);
+  if (rc == 0) rc = launch_after(long_count_kernel, grid, kLongThreads, st, a);
+  if (rc == 0) rc = launch_after(long_write_kernel, grid, kLongThreads, st, a);
+  return rc;
 }
 
 }  // namespace
 
-size_t evict_select_keys_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen) {
-  const int cs = cluster_of(max_seqlen);
-  if ((max_seqlen + cs - 1) / cs + 3 <= kKeysInSmem) return 0;
-  return sizeof(uint32_t) * (size_t)batch * rankings * (((size_t)max_seqlen + 3) / 4 * 4);
+size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen) {
+  return max_seqlen > kLongFrom ? long_layout((int64_t)batch * rankings, max_seqlen).total : 0;
 }
 
 int launch_evict_select(const EvictSelectArgs& a, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.max_seqlen > kLongFrom) return launch_long_select(a, st);
   const int cs = cluster_of(a.max_seqlen);
   const int R = a.per_group ? a.G : 1;
-  const int64_t per = ((int64_t)(a.max_seqlen + cs - 1) / cs + 3) / 4 * 4;
-  const int smem = (int)sizeof(SelCtl) + (int)sizeof(uint32_t) * (int)(per < kKeysInSmem ? per : kKeysInSmem);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(SelCtl) + 4 * kKeysInSmem);
-  if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)a.batch * R * cs));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -402,11 +738,13 @@ int launch_evict_select(const EvictSelectArgs& a, void* stream) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  const int gs = R == a.G ? 1 : a.G;
+  auto* kernel = cs > 1 ? (gs == 1 ? evict_select_kernel<true, 1> : gs == 2 ? evict_select_kernel<true, 2> : evict_select_kernel<true, 4>)
+                        : (gs == 1 ? evict_select_kernel<false, 1> : gs == 2 ? evict_select_kernel<false, 2> : evict_select_kernel<false, 4>);
   ProfScope p("evict_select", stream);
-  return (int)cudaLaunchKernelEx(&cfg, evict_select_kernel, a.weights, (int)a.G, (int)a.per_group, a.width, a.seqlens,
-                                 (int)a.max_seqlen, (int)a.budget, (int)a.n_sink, (int)a.n_recent, a.kept, a.new_lens,
-                                 a.keys, (int64_t)((a.max_seqlen + 3) / 4 * 4), a.err);
+  return (int)cudaLaunchKernelEx(&cfg, kernel, a.weights, (int)a.G, a.width, a.seqlens, (int)a.batch, (int)a.max_seqlen,
+                                 (int)a.budget, (int)a.n_sink, (int)a.n_recent, a.kept, a.new_lens, a.err);
 }
 
 int launch_evict_move(const EvictMoveArgs& m, void* stream) {

@@ -122,6 +122,23 @@ def test_keys_past_shared_memory(M, lens):
         assert new.cpu().tolist() == [min(n, budget) for n in lens]
 
 
+@pytest.mark.parametrize("per_group", [False, True])
+def test_long_and_short_in_one_batch(M, per_group):
+    # the longest decides the launch: rows that keep all, empty ones and bad lengths beside it
+    lens = [70001, 0, 100, 8192, 66000, 8193, 16384]
+    w = _weights(7, 2, 547, 21, "zeros")
+    for budget, sink, recent in ((100, 0, 100), (8192, 1, 5), (66000, 9, 9), (70003, 0, 0)):
+        _select(M, w, lens, budget, sink, recent, per_group)
+    shape = M.make_shape(8, 2, 64, 64, 16)
+    lens[3] = -1
+    with pytest.raises(M.MsaError, match="DEVICE_CHECK at site 261"):
+        M.msa_evict_select(shape, _pages(M, lens, 70001, 547), w.cuda(), 100, per_group=per_group)
+    kept, new = M.msa_evict_select(shape, _pages(M, lens, 70001, 547), w.cuda(), 100, per_group=per_group, check=False)
+    lens[3] = 0
+    assert new.cpu().tolist() == [min(n, 100) for n in lens]
+    np.testing.assert_array_equal(kept.cpu().numpy(), _want(w, lens, 100, 0, 0, per_group))
+
+
 def test_many_sequences(M):
     lens = [(i * 91) % 700 for i in range(600)]
     _select(M, _weights(600, 2, 6, 5), lens, 150, 2, 30, False)
