@@ -112,7 +112,7 @@ struct EvictSelectArgs {
   int32_t* kept;              // [batch, per_group ? G : 1, budget]
   int32_t* new_lens;          // [batch]
   void* work;                 // evict_select_work_bytes of workspace, right behind the header of err
-  DevError* err;              // cleared by the launcher
+  DevError* err;              // written in any case
 };
 // Workspace behind the header (0 where a sequence's keys fit in a cluster's shared memory).
 size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen);

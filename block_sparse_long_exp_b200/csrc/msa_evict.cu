@@ -36,8 +36,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPer = 8;                       // tokens of a thread, in its registers
-constexpr int kSelPart = kSelThreads * kSelPer;  // tokens of a CTA
+constexpr int kSelPart = kSelThreads * 8;        // tokens of a CTA at most: 4 or 8 a thread, in its registers
 constexpr int kMaxCluster = 4;
 constexpr uint32_t kForced = 0xffffffffu;        // above +inf's key
 
@@ -83,32 +82,34 @@ __device__ __forceinline__ void token_scores(const float* __restrict__ w, int64_
   for (int g = 0; g < GS; ++g)
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) v[g][q] = *reinterpret_cast<const uint4*>(w + g * width + 4 * q);
+  auto at = [&](int g, int i) {
+    const uint4 q = v[g][i / 4];
+    return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+  };
+  if constexpr (GS == 1) {
 #pragma unroll
-  for (int q = 0; q < N / 4; ++q)
+    for (int i = 0; i < N; ++i) u[i] = at(0, i);
+  } else {
+    uint32_t most = 0;                           // the largest size: from 0x7f800000 on an infinity or NaN is among them
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      uint32_t c[GS];
+    for (int i = 0; i < N; ++i) {
+      double s = scaled_down(at(0, i));
 #pragma unroll
-      for (int g = 0; g < GS; ++g) c[g] = x == 0 ? v[g][q].x : x == 1 ? v[g][q].y : x == 2 ? v[g][q].z : v[g][q].w;
-      if constexpr (GS == 1) {
-        u[4 * q + x] = c[0];
-      } else {
-        bool finite = true;
-        double s = 0.0;
+      for (int g = 1; g < GS; ++g) s += scaled_down(at(g, i));
+      u[i] = scaled_up(s);
 #pragma unroll
-        for (int g = 0; g < GS; ++g) {
-          finite &= (c[g] & 0x7f800000u) != 0x7f800000u;
-          s = g == 0 ? scaled_down(c[0]) : s + scaled_down(c[g]);
-        }
-        u[4 * q + x] = scaled_up(s);
-        if (!finite) {
-          double t = widen(__uint_as_float(c[0]));
+      for (int g = 0; g < GS; ++g) most = max(most, at(g, i) & 0x7fffffffu);
+    }
+    if (most >= 0x7f800000u) {
 #pragma unroll
-          for (int g = 1; g < GS; ++g) t += widen(__uint_as_float(c[g]));
-          u[4 * q + x] = __float_as_uint(narrow(t));
-        }
+      for (int i = 0; i < N; ++i) {
+        double s = widen(__uint_as_float(at(0, i)));
+#pragma unroll
+        for (int g = 1; g < GS; ++g) s += widen(__uint_as_float(at(g, i)));
+        u[i] = __float_as_uint(narrow(s));
       }
     }
+  }
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -138,16 +139,29 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   return incl - v + (warp == 0 ? 0u : before);
 }
 
-// Counts a bin (whole warps call).  A warp of one bin (weights that are all zero) adds once.
-__device__ __forceinline__ void count_bin(uint32_t* hist, uint32_t bin, bool in) {
-  const uint32_t m = __ballot_sync(0xffffffffu, in);
-  if (m == 0) return;
-  const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
-  if (__all_sync(0xffffffffu, !in || bin == first)) {
-    if ((threadIdx.x & 31) == 0) atomicAdd(&hist[first], __popc(m));
-  } else if (in) {
-    atomicAdd(&hist[bin], 1u);
+// Counts N bins a thread (whole warps call).  A warp of one bin (weights that
+// are all zero, the tokens kept in any case) adds once.
+template <int N>
+__device__ __forceinline__ void count_bins(uint32_t* hist, const uint32_t (&bin)[N], const bool (&in)[N]) {
+  uint32_t lo = 0xffffffffu, hi = 0u, c = 0;
+#pragma unroll
+  for (int x = 0; x < N; ++x)
+    if (in[x]) {
+      lo = min(lo, bin[x]);
+      hi = max(hi, bin[x]);
+      ++c;
+    }
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (c == 0) return;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lo == hi) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(&hist[lo], c);
+    return;
   }
+#pragma unroll
+  for (int x = 0; x < N; ++x)
+    if (in[x]) atomicAdd(&hist[bin[x]], 1u);
 }
 
 // Of 32 counts, a lane each, the lane in which the `need` first ones end, from the top; *above: those before it.
@@ -165,13 +179,18 @@ __device__ __forceinline__ int find_lane(uint32_t c, uint32_t need, uint32_t* ab
 }
 
 struct SelCtl {
-  uint32_t hist[3][2048];
-  uint32_t sum[2048];         // a cluster's histogram
+  union {
+    struct {
+      uint32_t hist[3][2048];
+      uint32_t sum[2048];     // a cluster's histogram
+    };
+    int32_t list[kSelPart];   // afterwards: the CTA's kept tokens in their order
+  };
   uint32_t warp_sum[kSelWarps];
   uint32_t gt, eq;            // this CTA's keys above and equal to the threshold
 };
 
-template <bool kCluster, int GS>
+template <bool kCluster, int GS, int PER>
 __global__ void __launch_bounds__(kSelThreads, 1)
 evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, const int32_t* __restrict__ seqlens,
                     int batch, int max_seqlen, int budget, int n_sink, int n_recent, int32_t* __restrict__ kept,
@@ -195,7 +214,7 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     if (lane == 0) ctl.warp_sum[warp] = bad;
     __syncthreads();
     if (warp == 0) {
-      bad = __reduce_min_sync(0xffffffffu, (int)ctl.warp_sum[lane]);
+      bad = __reduce_min_sync(0xffffffffu, lane < kSelWarps ? (int)ctl.warp_sum[lane] : batch);
       if (lane == 0)
         *err = bad < batch ? DevError{MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, bad, seqlens[bad]} : DevError{0, 0, 0, 0};
     }
@@ -206,18 +225,18 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     return;
   }
 
-  // ---- this CTA's tokens [j0, j0 + n), eight in a row to a thread
-  const int per = (L + cs - 1) / cs + (kSelPer - 1) & ~(kSelPer - 1);
+  // ---- this CTA's tokens [j0, j0 + n), PER in a row to a thread
+  const int per = (L + cs - 1) / cs + (PER - 1) & ~(PER - 1);
   const int j0 = min(rank * per, L), n = min(per, L - j0);
-  const int i0 = tid * kSelPer;
-  uint32_t key[kSelPer];
+  const int i0 = tid * PER;
+  uint32_t key[PER];
 #pragma unroll
-  for (int x = 0; x < kSelPer; ++x) key[x] = 0u;
+  for (int x = 0; x < PER; ++x) key[x] = 0u;
   if (i0 < n) token_scores<GS>(weights + ((int64_t)b * G + r) * width + j0 + i0, width, key);   // rows reach past L to their width
   for (int i = tid; i < 3 * 2048; i += kSelThreads) (&ctl.hist[0][0])[i] = 0u;
   __syncthreads();
 #pragma unroll
-  for (int x = 0; x < kSelPer; ++x) {
+  for (int x = 0; x < PER; ++x) {
     const int j = j0 + i0 + x;
     key[x] = (j < n_sink || j >= L - n_recent) ? kForced : order_key(key[x]);
   }
@@ -228,10 +247,14 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
   for (int pass = 0; pass < 3; ++pass) {
     constexpr int kShift[3] = {0, 21, 10}, kDown[3] = {21, 10, 0};
     uint32_t* hist = ctl.hist[pass];
+    uint32_t bins[PER];
+    bool in[PER];
 #pragma unroll
-    for (int x = 0; x < kSelPer; ++x)
-      count_bin(hist, key[x] >> kDown[pass] & (pass == 2 ? 1023u : 2047u),
-                i0 + x < n && (pass == 0 || key[x] >> kShift[pass] == top));
+    for (int x = 0; x < PER; ++x) {
+      bins[x] = key[x] >> kDown[pass] & (pass == 2 ? 1023u : 2047u);
+      in[x] = i0 + x < n && (pass == 0 || key[x] >> kShift[pass] == top);
+    }
+    count_bins(hist, bins, in);
     // a thread has two bins; every warp finds the bin from the warps' sums
     uint2 c = make_uint2(0u, 0u);
     if constexpr (kCluster) {
@@ -254,23 +277,22 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     const int at = find_lane(ctl.warp_sum[lane], need, &above);
     const uint2 d = reinterpret_cast<const uint2*>(hist)[32 * at + lane];
     const int bl = find_lane(d.x + d.y, need - above, &more);
-    const uint32_t upper = __shfl_sync(0xffffffffu, d.y, bl);
     need -= above + more;
+    const uint32_t upper = __shfl_sync(0xffffffffu, d.y, bl);
     const bool high = need <= upper;              // the upper of the lane's two bins
     if (!high) need -= upper;
-    const uint32_t bin = 64 * at + 2 * bl + (high ? 1 : 0);
-    top = top << (pass == 2 ? 10 : 11) | bin;
+    top = top << (pass == 2 ? 10 : 11) | (64 * at + 2 * bl + (high ? 1 : 0));
   }
   // keys above `top` all stay, and the first `need` of those equal to it
 
-  uint32_t f = 0;                                 // above | equal << 16 of the thread's eight
+  uint32_t f = 0;                                 // above | equal << 16 of the thread's tokens
 #pragma unroll
-  for (int x = 0; x < kSelPer; ++x)
+  for (int x = 0; x < PER; ++x)
     if (i0 + x < n) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
   uint32_t total;
   const uint32_t before = block_scan<kSelWarps>(f, ctl.warp_sum, &total);
-  uint32_t gt = before & 0xffffu, eq = before >> 16;
-  if constexpr (kCluster) {                       // and of the CTAs before this one
+  uint32_t eq0 = 0, first = 0;                    // equal keys of the CTAs before this one; kept tokens of theirs
+  if constexpr (kCluster) {
     if (tid == 0) {
       ctl.gt = total & 0xffffu;
       ctl.eq = total >> 16;
@@ -278,21 +300,29 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     cluster.sync();
     for (int k = 0; k < rank; ++k) {
       const SelCtl* other = cluster.map_shared_rank(&ctl, k);
-      gt += other->gt;
-      eq += other->eq;
+      first += other->gt;
+      eq0 += other->eq;
     }
+    first += min(eq0, need);
   }
+  // the list is put in order in shared memory (every histogram is read) and goes out in whole lines
+  const uint32_t left = need - min(eq0, need);    // equal keys that this CTA may keep
+  uint32_t gt = before & 0xffffu, eq = before >> 16;
 #pragma unroll
-  for (int x = 0; x < kSelPer; ++x) {
-    if (i0 + x >= n) break;
-    if (key[x] > top) {
-      dst[gt + min(eq, need)] = j0 + i0 + x;
-      ++gt;
-    } else if (key[x] == top) {
-      if (eq < need) dst[gt + eq] = j0 + i0 + x;
-      ++eq;
+  for (int x = 0; x < PER; ++x) {
+    if (i0 + x < n) {
+      if (key[x] > top) {
+        ctl.list[gt + min(eq, left)] = j0 + i0 + x;
+        ++gt;
+      } else if (key[x] == top) {
+        if (eq < left) ctl.list[gt + eq] = j0 + i0 + x;
+        ++eq;
+      }
     }
   }
+  __syncthreads();
+  const int kept_here = (int)((total & 0xffffu) + min(total >> 16, left));
+  for (int i = tid; i < kept_here; i += kSelThreads) dst[first + i] = ctl.list[i];
   if constexpr (kCluster) cluster.sync();         // the others read this CTA's counts
 }
 
@@ -367,23 +397,31 @@ struct LongPlace {
   }
 };
 
+// The histograms and the error word cleared, while the next kernel reads its weights.
+__global__ void __launch_bounds__(kLongThreads) long_clear_kernel(const LongArgs a) {
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = DevError{0, 0, 0, 0};
+  uint4* h = reinterpret_cast<uint4*>(a.hist);
+  for (int64_t i = blockIdx.x * kLongThreads + threadIdx.x; i < 3ll * a.rows * 512; i += gridDim.x * kLongThreads)
+    h[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int GS>
 __global__ void __launch_bounds__(kLongThreads) long_keys_kernel(const LongArgs a) {
   __shared__ uint32_t hist[2048];
   pdl_launch_dependents();
   const LongPlace p(a);
   const int tid = threadIdx.x;
-  if (p.part == 0 && p.r == 0 && tid == 0) {
-    a.new_lens[p.b] = p.L < a.budget ? p.L : a.budget;
-    if (p.L != a.seqlens[p.b]) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, p.b, a.seqlens[p.b]);
-  }
+  if (p.part == 0 && p.r == 0 && tid == 0) a.new_lens[p.b] = p.L < a.budget ? p.L : a.budget;
   if (!p.cut) {                                   // every token stays
+    pdl_wait();
+    if (p.part == 0 && p.r == 0 && tid == 0 && p.L != a.seqlens[p.b])
+      report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictSelect, p.b, a.seqlens[p.b]);
     int32_t* dst = a.kept + (int64_t)p.row * a.budget;
     for (int64_t i = p.part * kLongThreads + tid; i < a.budget; i += (int64_t)a.parts * kLongThreads)
       dst[i] = i < p.L ? (int32_t)i : -1;
     return;
   }
-  if (p.n == 0) return;
   for (int i = tid; i < 2048; i += kLongThreads) hist[i] = 0u;
   __syncthreads();
   const int j0 = p.part * kLongPart;
@@ -394,15 +432,20 @@ __global__ void __launch_bounds__(kLongThreads) long_keys_kernel(const LongArgs 
     const int i = (s * kLongThreads + tid) * 4;
     uint32_t u[4] = {0u, 0u, 0u, 0u};
     if (i < p.n) token_scores<GS>(w0 + i, a.width, u);               // the row reaches past L to its width
+    uint32_t bins[4];
+    bool in[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int j = j0 + i + x;
       u[x] = (j < a.n_sink || j >= p.L - a.n_recent) ? kForced : order_key(u[x]);
-      count_bin(hist, u[x] >> 21, i + x < p.n);
+      bins[x] = u[x] >> 21;
+      in[x] = i + x < p.n;
     }
+    count_bins(hist, bins, in);
     *reinterpret_cast<uint4*>(keys + i) = make_uint4(u[0], u[1], u[2], u[3]);   // past the part's end: not counted
   }
   __syncthreads();
+  pdl_wait();                                     // every CTA: this grid's end stands for the ends before it
   uint32_t* sum = a.hist + (int64_t)p.row * 2048;
   for (int i = tid; i < 2048; i += kLongThreads)
     if (hist[i] != 0) atomicAdd(&sum[i], hist[i]);
@@ -434,9 +477,14 @@ __global__ void __launch_bounds__(kLongThreads) long_hist_kernel(const LongArgs 
   for (int s = 0; s < kLongPer / 4; ++s) {
     const int i = (s * kLongThreads + tid) * 4;
     const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
+    uint32_t bins[4];
+    bool in[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      count_bin(hist, (u[x] >> kDown) & (kBins - 1), i + x < p.n && (u[x] >> kShift) == f.top);
+    for (int x = 0; x < 4; ++x) {
+      bins[x] = (u[x] >> kDown) & (kBins - 1);
+      in[x] = i + x < p.n && (u[x] >> kShift) == f.top;
+    }
+    count_bins(hist, bins, in);
   }
   __syncthreads();
   uint32_t* sum = a.hist + ((int64_t)PASS * a.rows + p.row) * 2048;
@@ -660,7 +708,8 @@ int cluster_of(int32_t max_seqlen) {
   return cs;
 }
 
-// From here on a (sequence, ranking) has a CTA per 8192 tokens and five launches: LONGNOTE
+// From here on a (sequence, ranking) has a CTA per 8192 tokens and six launches (18.7 us for 40K tokens where a
+// cluster of eight took 20.4 with one sequence and 36.7 with sixteen; a cluster of four takes 14.8 us for 20K).
 constexpr int32_t kLongFrom = kMaxCluster * kSelPart;
 
 struct LongLayout {
@@ -676,7 +725,7 @@ LongLayout long_layout(int64_t rows, int32_t max_seqlen) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  L.hist = take(sizeof(uint32_t) * 3 * rows * 2048);       // first: cleared with the header
+  L.hist = take(sizeof(uint32_t) * 3 * rows * 2048);
   L.found = take(sizeof(LongRow) * 3 * rows);
   L.counts = take(sizeof(uint2) * rows * L.parts);
   L.keys = take(sizeof(uint32_t) * rows * L.parts * (size_t)kLongPart);
@@ -689,8 +738,6 @@ int launch_long_select(const EvictSelectArgs& s, cudaStream_t st) {
   const int64_t rows = (int64_t)s.batch * R;
   const LongLayout L = long_layout(rows, s.max_seqlen);
   uint8_t* base = reinterpret_cast<uint8_t*>(s.work);
-  cudaError_t e = cudaMemsetAsync(s.err, 0, kWsHeader + sizeof(uint32_t) * 3 * rows * 2048, st);
-  if (e != cudaSuccess) return (int)e;
   LongArgs a{};
   a.weights = s.weights; a.width = s.width; a.seqlens = s.seqlens;
   a.G = s.G; a.R = R; a.parts = L.parts; a.max_seqlen = s.max_seqlen; a.budget = s.budget;
@@ -701,16 +748,16 @@ int launch_long_select(const EvictSelectArgs& s, cudaStream_t st) {
   a.counts = reinterpret_cast<uint2*>(base + L.counts);
   a.rows = (int32_t)rows; a.err = s.err;
   const dim3 grid((unsigned)(rows * L.parts));
-  {
+  const int64_t clear = (3 * rows * 512 + kLongThreads - 1) / kLongThreads;
+  long_clear_kernel<<<(unsigned)(clear < 592 ? clear : 592), kLongThreads, 0, st>>>(a);
+  int rc = (int)cudaGetLastError();
+  prof_count_launch(5);
+  if (rc == 0) {
     ProfScope p("evict_select", st);
-    if (R == s.G) long_keys_kernel<1><<<grid, kLongThreads, 0, st>>>(a);
-    else if (s.G == 2) long_keys_kernel<2><<<grid, kLongThreads, 0, st>>>(a);
-    else long_keys_kernel<4><<<grid, kLongThreads, 0, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return (int)e;
+    auto* keys = R == s.G ? long_keys_kernel<1> : s.G == 2 ? long_keys_kernel<2> : long_keys_kernel<4>;
+    rc = launch_after(keys, grid, kLongThreads, st, a);
   }
-  prof_count_launch(4);
-  int rc = launch_after(long_hist_kernel<1>, grid, kLongThreads, st, a);
+  if (rc == 0) rc = launch_after(long_hist_kernel<1>, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_hist_kernel<2>, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_count_kernel, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_write_kernel, grid, kLongThreads, st, a);
@@ -740,8 +787,10 @@ int launch_evict_select(const EvictSelectArgs& a, void* stream) {
   cfg.attrs = at;
   cfg.numAttrs = cs > 1 ? 1 : 0;
   const int gs = R == a.G ? 1 : a.G;
-  auto* kernel = cs > 1 ? (gs == 1 ? evict_select_kernel<true, 1> : gs == 2 ? evict_select_kernel<true, 2> : evict_select_kernel<true, 4>)
-                        : (gs == 1 ? evict_select_kernel<false, 1> : gs == 2 ? evict_select_kernel<false, 2> : evict_select_kernel<false, 4>);
+#define MSA_SELECT(C, P) \
+  (gs == 1 ? evict_select_kernel<C, 1, P> : gs == 2 ? evict_select_kernel<C, 2, P> : evict_select_kernel<C, 4, P>)
+  auto* kernel = cs > 1 ? MSA_SELECT(true, 8) : a.max_seqlen > 4 * kSelThreads ? MSA_SELECT(false, 8) : MSA_SELECT(false, 4);
+#undef MSA_SELECT
   ProfScope p("evict_select", stream);
   return (int)cudaLaunchKernelEx(&cfg, kernel, a.weights, (int)a.G, a.width, a.seqlens, (int)a.batch, (int)a.max_seqlen,
                                  (int)a.budget, (int)a.n_sink, (int)a.n_recent, a.kept, a.new_lens, a.err);
