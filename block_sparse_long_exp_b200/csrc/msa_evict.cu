@@ -7,17 +7,14 @@
 //   key T is found by its bits: 11, 11 and 10 at a time, a histogram of the keys
 //   that share the bits found so far.  Kept: the keys above T and, of those
 //   equal to T, the first ones.  Counts are whole numbers, so the result does
-//   not depend on the order of the atomics.  A cluster of 1 to 8 CTAs has one
-//   (sequence, ranking): each CTA counts its part of the tokens in its own
-//   shared memory and adds up the others' histograms from there; the histograms
-//   also give each part's number of kept tokens, so that every CTA knows where
-//   its tokens go.  Bound by latency (a few passes over shared memory with a
-//   cluster barrier after each) up to some 100,000 tokens, by the one pass over
-//   the weights in HBM beyond.
+//   not depend on the order of the atomics.  Up to 8192 tokens one CTA has a
+//   (sequence, ranking), the keys in its registers and the histograms in shared
+//   memory, and what it takes is the latency of some fifteen barriers; beyond,
+//   a CTA has 4096 tokens and the steps are launches.  Bound by those launches
+//   up to some 300,000 tokens in all, then by the weights from HBM.
 // move: the rows of the kept tokens gathered into other pages; reads and writes
 //   each kept byte once (HBM).  Out of place: a page of the source may be shared
 //   with another sequence, and the rows can go in any order.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -27,8 +24,6 @@
 #include "msa_gather.h"
 #include "msa_internal.h"
 
-namespace cg = cooperative_groups;
-
 namespace msa {
 namespace {
 
@@ -37,7 +32,6 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelPart = kSelThreads * 8;        // tokens of a CTA at most: 4 or 8 a thread, in its registers
-constexpr int kMaxCluster = 4;
 constexpr uint32_t kForced = 0xffffffffu;        // above +inf's key
 
 // 32-bit key in the order of the scores; NaN lowest, -0 as 0.
@@ -180,32 +174,26 @@ __device__ __forceinline__ int find_lane(uint32_t c, uint32_t need, uint32_t* ab
 
 struct SelCtl {
   union {
-    struct {
-      uint32_t hist[3][2048];
-      uint32_t sum[2048];     // a cluster's histogram
-    };
-    int32_t list[kSelPart];   // afterwards: the CTA's kept tokens in their order
+    uint32_t hist[3][2048];
+    int32_t list[kSelPart];   // afterwards: the kept tokens in their order
   };
   uint32_t warp_sum[kSelWarps];
-  uint32_t gt, eq;            // this CTA's keys above and equal to the threshold
 };
 
-template <bool kCluster, int GS, int PER>
+// A CTA per (sequence, ranking).
+template <int GS, int PER>
 __global__ void __launch_bounds__(kSelThreads, 1)
 evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, const int32_t* __restrict__ seqlens,
                     int batch, int max_seqlen, int budget, int n_sink, int n_recent, int32_t* __restrict__ kept,
                     int32_t* __restrict__ new_lens, DevError* err) {
   __shared__ SelCtl ctl;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int cs = kCluster ? cluster.num_blocks() : 1, rank = kCluster ? cluster.block_rank() : 0;
   const int R = GS == 1 ? G : 1;
-  const int row = blockIdx.x / cs;                // (sequence, ranking)
-  const int b = row / R, r = row - b * R;
+  const int row = blockIdx.x, b = row / R, r = row - b * R;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bounded = [&](int n) { return n < 0 || n > max_seqlen ? 0 : n; };
   const int L = bounded(seqlens[b]);
   int32_t* dst = kept + (int64_t)row * budget;
-  if (rank == 0 && tid == 0 && r == 0) new_lens[b] = L < budget ? L : budget;
+  if (tid == 0 && r == 0) new_lens[b] = L < budget ? L : budget;
   if (blockIdx.x == 0) {                          // the first bad length, or none
     int bad = batch;
     for (int i = tid; i < batch; i += kSelThreads)
@@ -220,24 +208,22 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     }
     __syncthreads();
   }
-  if (L <= budget) {                              // every token stays (the whole cluster takes this way)
-    for (int64_t i = rank * kSelThreads + tid; i < budget; i += cs * kSelThreads) dst[i] = i < L ? (int32_t)i : -1;
+  if (L <= budget) {                              // every token stays
+    for (int64_t i = tid; i < budget; i += kSelThreads) dst[i] = i < L ? (int32_t)i : -1;
     return;
   }
 
-  // ---- this CTA's tokens [j0, j0 + n), PER in a row to a thread
-  const int per = (L + cs - 1) / cs + (PER - 1) & ~(PER - 1);
-  const int j0 = min(rank * per, L), n = min(per, L - j0);
+  // ---- PER tokens in a row to a thread
   const int i0 = tid * PER;
   uint32_t key[PER];
 #pragma unroll
   for (int x = 0; x < PER; ++x) key[x] = 0u;
-  if (i0 < n) token_scores<GS>(weights + ((int64_t)b * G + r) * width + j0 + i0, width, key);   // rows reach past L to their width
+  if (i0 < L) token_scores<GS>(weights + ((int64_t)b * G + r) * width + i0, width, key);   // rows reach past L to their width
   for (int i = tid; i < 3 * 2048; i += kSelThreads) (&ctl.hist[0][0])[i] = 0u;
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    const int j = j0 + i0 + x;
+    const int j = i0 + x;
     key[x] = (j < n_sink || j >= L - n_recent) ? kForced : order_key(key[x]);
   }
 
@@ -252,24 +238,12 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
       bins[x] = key[x] >> kDown[pass] & (pass == 2 ? 1023u : 2047u);
-      in[x] = i0 + x < n && (pass == 0 || key[x] >> kShift[pass] == top);
+      in[x] = i0 + x < L && (pass == 0 || key[x] >> kShift[pass] == top);
     }
     count_bins(hist, bins, in);
     // a thread has two bins; every warp finds the bin from the warps' sums
-    uint2 c = make_uint2(0u, 0u);
-    if constexpr (kCluster) {
-      cluster.sync();
-      for (int k = 0; k < cs; ++k) {
-        const uint2 v = reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, k))[tid];
-        c.x += v.x;
-        c.y += v.y;
-      }
-      reinterpret_cast<uint2*>(ctl.sum)[tid] = c;
-      hist = ctl.sum;
-    } else {
-      __syncthreads();
-      c = reinterpret_cast<const uint2*>(hist)[tid];
-    }
+    __syncthreads();
+    const uint2 c = reinterpret_cast<const uint2*>(hist)[tid];
     const uint32_t w = __reduce_add_sync(0xffffffffu, c.x + c.y);
     if (lane == 0) ctl.warp_sum[warp] = w;
     __syncthreads();
@@ -288,53 +262,36 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
   uint32_t f = 0;                                 // above | equal << 16 of the thread's tokens
 #pragma unroll
   for (int x = 0; x < PER; ++x)
-    if (i0 + x < n) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
+    if (i0 + x < L) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
   uint32_t total;
   const uint32_t before = block_scan<kSelWarps>(f, ctl.warp_sum, &total);
-  uint32_t eq0 = 0, first = 0;                    // equal keys of the CTAs before this one; kept tokens of theirs
-  if constexpr (kCluster) {
-    if (tid == 0) {
-      ctl.gt = total & 0xffffu;
-      ctl.eq = total >> 16;
-    }
-    cluster.sync();
-    for (int k = 0; k < rank; ++k) {
-      const SelCtl* other = cluster.map_shared_rank(&ctl, k);
-      first += other->gt;
-      eq0 += other->eq;
-    }
-    first += min(eq0, need);
-  }
   // the list is put in order in shared memory (every histogram is read) and goes out in whole lines
-  const uint32_t left = need - min(eq0, need);    // equal keys that this CTA may keep
   uint32_t gt = before & 0xffffu, eq = before >> 16;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    if (i0 + x < n) {
+    if (i0 + x < L) {
       if (key[x] > top) {
-        ctl.list[gt + min(eq, left)] = j0 + i0 + x;
+        ctl.list[gt + min(eq, need)] = i0 + x;
         ++gt;
       } else if (key[x] == top) {
-        if (eq < left) ctl.list[gt + eq] = j0 + i0 + x;
+        if (eq < need) ctl.list[gt + eq] = i0 + x;
         ++eq;
       }
     }
   }
   __syncthreads();
-  const int kept_here = (int)((total & 0xffffu) + min(total >> 16, left));
-  for (int i = tid; i < kept_here; i += kSelThreads) dst[first + i] = ctl.list[i];
-  if constexpr (kCluster) cluster.sync();         // the others read this CTA's counts
+  for (int i = tid; i < budget; i += kSelThreads) dst[i] = ctl.list[i];
 }
 
 // -------------------------------------------------- select, long sequences ---
 //
-// The same search with a CTA per 8192 tokens of every (sequence, ranking), the
+// The same search with a CTA per 4096 tokens of every (sequence, ranking), the
 // histograms in global memory and a launch per step: the keys and the histogram
 // of their top 11 bits; of the next 11; of the last 10; each part's numbers of
 // kept tokens; the kept tokens.  Every CTA finds the step's bin by itself.
 
 constexpr int kLongThreads = 512;
-constexpr int kLongPart = 8192;                   // tokens per CTA
+constexpr int kLongPart = 4096;                   // tokens per CTA
 constexpr int kLongPer = kLongPart / kLongThreads;
 
 struct LongRow {
@@ -347,7 +304,7 @@ struct LongArgs {
   int32_t G, R, parts, max_seqlen, budget, n_sink, n_recent;
   int32_t* kept;
   int32_t* new_lens;
-  uint32_t* keys;             // [rows, parts * 8192]
+  uint32_t* keys;             // [rows, parts * 4096]
   uint32_t* hist;             // [3, rows, 2048], zeroed
   LongRow* found;             // [3, rows]
   uint2* counts;              // [rows, parts]: keys above and equal to the threshold
@@ -525,6 +482,7 @@ __global__ void __launch_bounds__(kLongThreads) long_count_kernel(const LongArgs
 
 __global__ void __launch_bounds__(kLongThreads) long_write_kernel(const LongArgs a) {
   __shared__ uint32_t warp_sum[kLongThreads / 32];
+  __shared__ int32_t list[kLongPart];             // the part's kept tokens: they go out in whole lines
   const LongPlace p(a);
   const int tid = threadIdx.x;
   pdl_wait();
@@ -552,25 +510,29 @@ __global__ void __launch_bounds__(kLongThreads) long_write_kernel(const LongArgs
       if (tid * kLongPer + 4 * s + x < p.n) c += u[x] > f.top ? 1u : (u[x] == f.top ? 0x10000u : 0u);
   }
   const uint32_t before = block_scan<kLongThreads / 32>(c, warp_sum, &total);
-  gt += before & 0xffffu;
-  eq += before >> 16;
-  int32_t* dst = a.kept + (int64_t)p.row * a.budget;
+  const uint32_t taken = min(eq, f.need), left = f.need - taken;   // equal keys kept by the parts before, and still to keep
+  uint32_t g1 = before & 0xffffu, e1 = before >> 16;
   const int j0 = p.part * kLongPart + tid * kLongPer;
 #pragma unroll
   for (int s = 0; s < kLongPer / 4; ++s) {
     const uint32_t u[4] = {k[s].x, k[s].y, k[s].z, k[s].w};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      if (tid * kLongPer + 4 * s + x >= p.n) break;
-      if (u[x] > f.top) {
-        dst[gt + min(eq, f.need)] = j0 + 4 * s + x;
-        ++gt;
-      } else if (u[x] == f.top) {
-        if (eq < f.need) dst[gt + eq] = j0 + 4 * s + x;
-        ++eq;
+      if (tid * kLongPer + 4 * s + x < p.n) {
+        if (u[x] > f.top) {
+          list[g1 + min(e1, left)] = j0 + 4 * s + x;
+          ++g1;
+        } else if (u[x] == f.top) {
+          if (e1 < left) list[g1 + e1] = j0 + 4 * s + x;
+          ++e1;
+        }
       }
     }
   }
+  __syncthreads();
+  int32_t* dst = a.kept + (int64_t)p.row * a.budget + gt + taken;
+  const int here = (int)((total & 0xffffu) + min(total >> 16, left));
+  for (int i = tid; i < here; i += kLongThreads) dst[i] = list[i];
 }
 
 // ------------------------------------------------------------------- move ---
@@ -701,16 +663,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   }
 }
 
-// CTAs per (sequence, ranking).
-int cluster_of(int32_t max_seqlen) {
-  int cs = 1;
-  while (cs < kMaxCluster && max_seqlen > cs * kSelPart) cs *= 2;
-  return cs;
-}
-
-// From here on a (sequence, ranking) has a CTA per 8192 tokens and six launches (18.7 us for 40K tokens where a
-// cluster of eight took 20.4 with one sequence and 36.7 with sixteen; a cluster of four takes 14.8 us for 20K).
-constexpr int32_t kLongFrom = kMaxCluster * kSelPart;
+// Beyond one CTA's tokens a (sequence, ranking) has a CTA per 4096 and six
+// launches: 13.6 us for 10K to 200K tokens, where a cluster of CTAs with the
+// histograms in shared memory took 13.2 for 10K, 14.8 for 20K and 20.4 for 40K;
+// one CTA takes 8.9 us for 5K.
+constexpr int32_t kLongFrom = kSelPart;
 
 struct LongLayout {
   int32_t parts;
@@ -773,27 +730,14 @@ size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seql
 int launch_evict_select(const EvictSelectArgs& a, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.max_seqlen > kLongFrom) return launch_long_select(a, st);
-  const int cs = cluster_of(a.max_seqlen);
-  const int R = a.per_group ? a.G : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.batch * R * cs));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  const int gs = R == a.G ? 1 : a.G;
-#define MSA_SELECT(C, P) \
-  (gs == 1 ? evict_select_kernel<C, 1, P> : gs == 2 ? evict_select_kernel<C, 2, P> : evict_select_kernel<C, 4, P>)
-  auto* kernel = cs > 1 ? MSA_SELECT(true, 8) : a.max_seqlen > 4 * kSelThreads ? MSA_SELECT(false, 8) : MSA_SELECT(false, 4);
+  const int gs = a.per_group ? 1 : a.G;
+#define MSA_SELECT(P) (gs == 1 ? evict_select_kernel<1, P> : gs == 2 ? evict_select_kernel<2, P> : evict_select_kernel<4, P>)
+  auto* kernel = a.max_seqlen > 4 * kSelThreads ? MSA_SELECT(8) : MSA_SELECT(4);   // 1K tokens: 6.2 us with 4, 8.7 with 8
 #undef MSA_SELECT
   ProfScope p("evict_select", stream);
-  return (int)cudaLaunchKernelEx(&cfg, kernel, a.weights, (int)a.G, a.width, a.seqlens, (int)a.batch, (int)a.max_seqlen,
-                                 (int)a.budget, (int)a.n_sink, (int)a.n_recent, a.kept, a.new_lens, a.err);
+  kernel<<<(unsigned)(a.batch * (a.per_group ? a.G : 1)), kSelThreads, 0, st>>>(
+      a.weights, a.G, a.width, a.seqlens, a.batch, a.max_seqlen, a.budget, a.n_sink, a.n_recent, a.kept, a.new_lens, a.err);
+  return (int)cudaGetLastError();
 }
 
 int launch_evict_move(const EvictMoveArgs& m, void* stream) {

@@ -88,7 +88,7 @@ def test_choice_among_odd_values(M, kind):
             _select(M, w, lens, budget, sink, recent, per_group)
 
 
-@pytest.mark.parametrize("L", [4095, 4096, 4097, 8192, 8193, 16385, 32770, 65537, 70001])
+@pytest.mark.parametrize("L", [4095, 4096, 4097, 8191, 8192, 8193, 12289, 16385, 32770, 65537, 70001])
 def test_parts_of_a_long_sequence(M, L):
     blocks = -(-L // PAGE)
     for kind, budget in (("spread", L // 3), ("ties", L // 2), ("zeros", L - 1)):
