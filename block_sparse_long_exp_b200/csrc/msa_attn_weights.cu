@@ -24,6 +24,8 @@
 //           adds them in the order of the CTAs: the same from run to run.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "msa_common.cuh"
 #include "msa_cache.h"
 #include "msa_internal.h"
@@ -31,10 +33,10 @@
 namespace msa {
 namespace {
 
-constexpr int kAwThreads = 384;
+constexpr int kAwSumWarps = 8;                    // a lane of TMEM, that is a key, to a thread
+constexpr int kAwThreads = 32 * (4 + kAwSumWarps);
 constexpr int kAwKeys = 256;                      // keys of a unit
 constexpr int kAwCols = 128;                      // (query, head) columns of a unit
-constexpr int kAwLse = 3;                         // stages of the columns' log-sum-exps
 constexpr uint32_t kAwTmem = 512;                 // 2 units x 2 halves of the keys x 128 columns
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -48,7 +50,6 @@ __host__ __device__ constexpr int num_q() { return D == 128 ? 3 : 8; }
 struct AwCtl {
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[8], q_empty[8];
-  uint64_t l_full[kAwLse], l_empty[kAwLse];
   uint64_t s_full[2], s_free[2];
   uint64_t mma_done;
   int64_t warp_sum[kAwThreads / 32];
@@ -57,6 +58,63 @@ struct AwCtl {
   uint32_t tmem_base;
   int32_t abort_flag;
 };
+
+// ---- 2^x for pairs of 32-bit numbers ----
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {   // NaN stays NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(hi));
+  return r;
+}
+// acc += 2^x without the exponential's unit: x = i + f with i whole and |f| <=
+// 1/2, 2^f a polynomial of degree 5 (fitted to the smallest largest relative
+// error over [-1/2, 1/2]: 2^-23.7, with the roundings 2^-22.2; the unit's own
+// is 2^-22), and 2^i a number whose exponent field is i + 127: what x + 3 2^22 +
+// 127 has in its low bits.  Below -127 the result is 0, from 127.5 on infinite.
+__device__ __forceinline__ uint64_t add_exp2_poly(uint64_t x, uint64_t acc) {
+  float a, b;
+  unpair(x, a, b);
+  x = pair(clamp_nan(a, -127.f, 128.f), clamp_nan(b, -127.f, 128.f));
+  const uint64_t magic = pair(12583039.f, 12583039.f), back = pair(-12583039.f, -12583039.f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t i = add2(t, back);
+  const uint64_t f = fma2(i, pair(-1.f, -1.f), x);
+  uint64_t p = pair(0.001327647129073739f, 0.001327647129073739f);
+  p = fma2(p, f, pair(0.009675540961325169f, 0.009675540961325169f));
+  p = fma2(p, f, pair(0.05550713092088699f, 0.05550713092088699f));
+  p = fma2(p, f, pair(0.24022120237350464f, 0.24022120237350464f));
+  p = fma2(p, f, pair(0.6931469440460205f, 0.6931469440460205f));
+  p = fma2(p, f, pair(1.f, 1.f));
+  unpair(t, a, b);
+  return fma2(p, pair(__uint_as_float(__float_as_uint(a) << 23), __uint_as_float(__float_as_uint(b) << 23)), acc);
+}
+// Of eight pairs of columns the ones whose exponentials take that way.
+constexpr uint32_t kByPolynomial = 0x12;          // 2 of 8
+__device__ __forceinline__ uint64_t add_exp2(uint64_t x, uint64_t acc, int at) {   // `at` a constant once unrolled
+  if ((kByPolynomial >> at) & 1u) return add_exp2_poly(x, acc);
+  float a, b;
+  unpair(x, a, b);
+  return add2(acc, pair(ex2_approx(a), ex2_approx(b)));
+}
 
 // The units of one sequence: T queries that are the last of S tokens, key blocks
 // of 256, column tiles of qt queries.  Block i is seen from column tile
@@ -163,29 +221,38 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const float* __restrict__ lse, float* __restrict__ weights, int64_t width, float decay, int batch,
                     int H, int G, int qt_log, float scale_log2, const int32_t* __restrict__ cu_q,
                     const int32_t* __restrict__ cu_k, AwOpen* __restrict__ open, float* __restrict__ part,
-                    DevError* err) {
+                    DevError* errors) {
   constexpr int NQ = num_q<D>();
   constexpr int KST = k_stage<D>(), QST = q_stage<D>();
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  // the swizzled tiles want 1024-byte boundaries; there is no room to round up (this kernel has no other shared memory)
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* k_s = smem;                            // 2 stages of 256 keys
   uint8_t* q_s = k_s + 2 * KST;                   // NQ stages of 128 columns
   float* l_s = reinterpret_cast<float*>(q_s + NQ * QST);
-  AwCtl* ctl = reinterpret_cast<AwCtl*>(l_s + kAwLse * kAwCols);
+  AwCtl* ctl = reinterpret_cast<AwCtl*>(l_s + 2 * kAwCols);
   volatile int32_t* abort_flag = &ctl->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hg = H / G, hg_log = 7 - qt_log;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits for this grid's end
+  DevError* err = errors + blockIdx.x;            // the join makes one word of them
+  const bool placed = (smem_u32(smem) & 1023u) == 0;
+  if (tid == 0) {
+    *err = placed ? DevError{0, 0, 0, 0} : DevError{MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, -1, -1};
+    open[blockIdx.x] = AwOpen{-1, 0, 0, 0};       // until the run is known to leave a block open
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_q);
+  }
+  if (!placed) return;                            // never seen
 
   // ---- this CTA's run: one scan over the sequences' numbers of units
   {
     const int per = (batch + kAwThreads - 1) / kAwThreads;
     const int b0 = tid * per, b1 = min(b0 + per, batch);
     int64_t sum = 0;
+    int bad = -1;
     for (int b = b0; b < b1; ++b) {
       const int T = cu_q[b + 1] - cu_q[b], S = cu_k[b + 1] - cu_k[b];
-      if (blockIdx.x == 0 && (T < 0 || T > S)) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, b, T);
+      if (T < 0 || T > S) bad = b;
       sum += G * SeqUnits(T, S, qt_log).per_group;
     }
     int64_t incl = sum;
@@ -196,26 +263,22 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
     if (lane == 31) ctl->warp_sum[warp] = incl;
     if (tid == 0) {
-      open[blockIdx.x] = AwOpen{-1, 0, 0, 0};     // until the run is known to leave a block open
       for (int i = 0; i < 2; ++i) {
         mbar_init(&ctl->k_full[i], 1);
         mbar_init(&ctl->k_empty[i], 1);
-        mbar_init(&ctl->s_full[i], 1);
-        mbar_init(&ctl->s_free[i], 8);
+        mbar_init(&ctl->s_full[i], 2);            // the products and the columns' log-sum-exps
+        mbar_init(&ctl->s_free[i], kAwSumWarps);
       }
       for (int i = 0; i < NQ; ++i) {
         mbar_init(&ctl->q_full[i], 1);
         mbar_init(&ctl->q_empty[i], 1);
-      }
-      for (int i = 0; i < kAwLse; ++i) {
-        mbar_init(&ctl->l_full[i], 1);
-        mbar_init(&ctl->l_empty[i], 8);
       }
       mbar_init(&ctl->mma_done, 1);
       ctl->abort_flag = 0;
       fence_mbar_init();
     }
     __syncthreads();
+    if (blockIdx.x == 0 && bad >= 0) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, bad, cu_q[bad + 1] - cu_q[bad]);
     int64_t before = 0, total = 0;
     for (int w = 0; w < kAwThreads / 32; ++w) {
       if (w < warp) before += ctl->warp_sum[w];
@@ -252,8 +315,6 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (warp == 0) {
     // -------------------------------------------------------------- loads
     if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_q);
       Walk w;
       w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
       bool ok = true;
@@ -350,16 +411,16 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (t + 1 < w.block_end()) ++w.ct; else w.next_block();
         fetch(next);
       }
-      const int st = n % kAwLse;
-      if (lane == 0) ok = !*abort_flag && mbar_wait(&ctl->l_empty[st], ((n / kAwLse) + 1) & 1);
+      const int st = n & 1;
+      if (lane == 0) ok = !*abort_flag && mbar_wait(&ctl->s_free[st], ((n >> 1) + 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
-      // a log-sum-exp of -inf (nothing seen) as +inf: every 2^(s - inf) is 0
-      auto scaled = [](float l) { return l == -INFINITY ? INFINITY : l * kLog2e; };
+      // (negated; a log-sum-exp of -inf, nothing seen, as +inf: every 2^(s - inf) is 0)
+      auto scaled = [](float l) { return l == -INFINITY ? -INFINITY : l * -kLog2e; };
       reinterpret_cast<float4*>(l_s + st * kAwCols)[lane] =
           make_float4(scaled(v.x), scaled(v.y), scaled(v.z), scaled(v.w));
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->l_full[st]);
+      if (lane == 0) mbar_arrive(&ctl->s_full[st]);
       v = next;
     }
     if (!ok && lane == 0) {
@@ -371,64 +432,78 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int half = (warp - 4) >> 2;
     const int key = half * 128 + 32 * (warp & 3) + lane;             // in the unit
     const uint32_t col0 = tmem + half * 128 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint64_t scale2 = pair(scale_log2, scale_log2);
     Walk w;
     w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
     int n = 0;
     bool ok = true;
     for (int64_t t = lo; t < hi && ok;) {
-      const int64_t t0 = t, end = w.block_end(), e = min(hi, end);
+      const int64_t t0 = t, end = w.block_end();
+      const int units = (int)(min(hi, end) - t);
       const int j = w.kb * kAwKeys + key;                             // position of this thread's key
       const int first_q = j - (w.u.S - w.u.T);                        // the first query that sees it
+      // tiles from here to there count whole for the warp's 32 keys
+      const int whole_from = (max(first_q - lane + 31, 0) + (1 << qt_log) - 1) >> qt_log, whole_to = w.u.T >> qt_log;
       float acc = 0.f, comp = 0.f;                                    // compensated: up to millions of terms
-      for (; t < e; ++t, ++n, ++w.ct) {
-        const int slot = n & 1, st = n % kAwLse;
-        ok = !*abort_flag && mbar_wait(&ctl->l_full[st], (n / kAwLse) & 1) && mbar_wait(&ctl->s_full[slot], (n >> 1) & 1);
+      for (int k = 0; k < units; ++k, ++n, ++w.ct) {
+        const int slot = n & 1;
+        ok = mbar_wait(&ctl->s_full[slot], (n >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int q0 = w.ct << qt_log;
-        // columns [xlo, xhi) count for this key
-        const int xlo = first_q > q0 ? min(first_q - q0, 128) << hg_log : 0;
-        const int xhi = min((w.u.T - q0) << hg_log, kAwCols);
-        const bool all = __all_sync(0xffffffffu, xlo == 0) && xhi == kAwCols;
-        const float4* lv = reinterpret_cast<const float4*>(l_s + st * kAwCols);
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c = 0; c < kAwCols; c += 32) {
-          if (c >= xhi) break;
-          uint32_t r[32];
-          tmem_ld32(col0 + slot * 256 + c, r);
-          tmem_ld_wait();
-          if (all) {
+        const float* lv = l_s + slot * kAwCols;
+        const uint32_t col = col0 + slot * 256;
+        uint64_t s0 = 0, s1 = 0;                                      // pairs of 0.f
+        if (w.ct >= whole_from && w.ct < whole_to) {
+          uint32_t r[2][32];
+          tmem_ld32(col, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld32(col + 32 * (c + 1), r[(c + 1) & 1]);  // on its way meanwhile
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
-              const float4 l = lv[(c + x) >> 2];
-              s[0] += ex2_approx(fmaf(__uint_as_float(r[x]), scale_log2, -l.x));
-              s[1] += ex2_approx(fmaf(__uint_as_float(r[x + 1]), scale_log2, -l.y));
-              s[2] += ex2_approx(fmaf(__uint_as_float(r[x + 2]), scale_log2, -l.z));
-              s[3] += ex2_approx(fmaf(__uint_as_float(r[x + 3]), scale_log2, -l.w));
+              const uint32_t* v = r[c & 1] + x;
+              const float4 l = *reinterpret_cast<const float4*>(lv + 32 * c + x);
+              const uint64_t a = fma2(pair(__uint_as_float(v[0]), __uint_as_float(v[1])), scale2, pair(l.x, l.y));
+              const uint64_t b = fma2(pair(__uint_as_float(v[2]), __uint_as_float(v[3])), scale2, pair(l.z, l.w));
+              s0 = add_exp2(a, s0, x / 2 % 8);
+              s1 = add_exp2(b, s1, x / 2 % 8 + 1);
             }
-          } else {
+          }
+        } else {
+          // columns [xlo, xhi) count for this key; what the others hold does not
+          const int q0 = w.ct << qt_log;
+          const int xlo = first_q > q0 ? min(first_q - q0, 128) << hg_log : 0;
+          const int xhi = min((w.u.T - q0) << hg_log, kAwCols);
+          const int none = __shfl_sync(0xffffffffu, xlo, 0);          // the warp's first key sees the most
+#pragma unroll 1
+          for (int c = none & ~31; c < xhi; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(col + c, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float p = ex2_approx(fmaf(__uint_as_float(r[x]), scale_log2, -l_s[st * kAwCols + c + x]));
-              s[x & 3] += (c + x >= xlo && c + x < xhi) ? p : 0.f;    // what a masked column holds does not count
+            for (int x = 0; x < 32; x += 2) {
+              const float p = ex2_approx(fmaf(__uint_as_float(r[x]), scale_log2, lv[c + x]));
+              const float q = ex2_approx(fmaf(__uint_as_float(r[x + 1]), scale_log2, lv[c + x + 1]));
+              s0 = add2(s0, pair(c + x >= xlo && c + x < xhi ? p : 0.f, c + x + 1 >= xlo && c + x + 1 < xhi ? q : 0.f));
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->s_free[slot]);
-          mbar_arrive(&ctl->l_empty[st]);
-        }
+        if (lane == 0) mbar_arrive(&ctl->s_free[slot]);
+        float s[4];
+        unpair(s0, s[0], s[1]);
+        unpair(s1, s[2], s[3]);
         const float y = ((s[0] + s[1]) + (s[2] + s[3])) - comp, z = acc + y;
         comp = (z - acc) - y;
         acc = z;
       }
       if (!ok) break;
-      // the block's sums: whole ones are written, others left for the join
-      if (t0 == w.kb_first && e == end) {
+      t += units;
+      // whole blocks' sums are written, others left for the join
+      if (t0 == w.kb_first && t == end) {
         if (j < w.u.S) {
           float* dst = weights + ((int64_t)w.b * G + w.g) * width + j;
           *dst = decayed(decay, dst, acc);
@@ -436,7 +511,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       } else {
         part[((int64_t)blockIdx.x * 2 + (t0 == w.kb_first ? 1 : 0)) * kAwKeys + key] = acc;
       }
-      if (t0 == w.kb_first && e < end && warp == 4 && lane == 0)
+      if (t0 == w.kb_first && t < end && warp == 4 && lane == 0)
         open[blockIdx.x] = AwOpen{w.b, w.g, w.kb, run_of(end - 1, total, gridDim.x)};
       if (t < hi) w.next_block();
     }
@@ -453,11 +528,20 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
 }
 
-// Adds the parts of the key block that begins in run i and ends in another.
+// Adds the parts of the key block that begins in run i and ends in another, and
+// makes one error word of the CTAs'.
 __global__ void __launch_bounds__(kAwKeys)
 weights_join_kernel(const AwOpen* __restrict__ open, const float* __restrict__ part, float* __restrict__ weights,
-                    int64_t width, float decay, int G, const int32_t* __restrict__ cu_k) {
+                    int64_t width, float decay, int G, const int32_t* __restrict__ cu_k,
+                    const DevError* __restrict__ errors, DevError* __restrict__ err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x < 32) {      // the first CTA's that found something
+    int first = gridDim.x;
+    for (int i = threadIdx.x; i < gridDim.x; i += 32)
+      if (errors[i].code != 0) first = min(first, i);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (threadIdx.x == 0) *err = first < gridDim.x ? errors[first] : DevError{0, 0, 0, 0};
+  }
   const AwOpen o = open[blockIdx.x];
   if (o.b < 0) return;
   const int j = o.kb * kAwKeys + threadIdx.x;
@@ -487,16 +571,16 @@ int launch_units(const AttnWeightsArgs& a, int ctas, cudaStream_t st) {
     const int rc = make_tmap_bf16(&tm_q, a.q, 3, dims, strides, box, 128);
     if (rc != 0) return rc;
   }
-  constexpr int smem = 1024 + 2 * k_stage<D>() + num_q<D>() * q_stage<D>() + kAwLse * kAwCols * 4 + (int)sizeof(AwCtl);
+  constexpr int smem = 2 * k_stage<D>() + num_q<D>() * q_stage<D>() + 2 * kAwCols * 4 + (int)sizeof(AwCtl);
   static_assert(smem <= 232448, "shared memory of one CTA");
   static_assert(num_q<D>() <= 8, "barriers of the query stages");
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return (int)e;
+  static std::atomic<uint64_t> ready{0};
+  const int rc = allow_smem(attn_weights_kernel<D>, smem, &ready);
+  if (rc != 0) return rc;
   ProfScope p("attn_weights", st);
   attn_weights_kernel<D><<<ctas, kAwThreads, smem, st>>>(
       tm_k, tm_q, a.lse, a.weights, a.width, a.decay, a.batch, a.H, a.G, qt_log, a.sm_scale * kLog2e, a.cu_q, a.cu_k,
-      static_cast<AwOpen*>(a.open), a.part, a.err);
+      static_cast<AwOpen*>(a.open), a.part, a.errors);
   return (int)cudaGetLastError();
 }
 
@@ -504,7 +588,8 @@ int launch_units(const AttnWeightsArgs& a, int ctas, cudaStream_t st) {
 
 AttnWeightsLayout attn_weights_layout() {
   AttnWeightsLayout L{};
-  L.open = kWsHeader;
+  L.errors = kWsHeader;
+  L.open = align_up(L.errors + sizeof(DevError) * kDecodeCtas, 256);
   L.part = align_up(L.open + sizeof(AwOpen) * kDecodeCtas, 256);
   L.total = align_up(L.part + sizeof(float) * (size_t)kDecodeCtas * 2 * kAwKeys, 256);
   return L;
@@ -519,18 +604,9 @@ int launch_attn_weights(const AttnWeightsArgs& a, void* stream) {
   const int ctas = sms < kDecodeCtas ? sms : kDecodeCtas;
   const int rc = a.d == 128 ? launch_units<128>(a, ctas, st) : launch_units<64>(a, ctas, st);
   if (rc != 0) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kAwKeys);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   ProfScope p("attn_weights_join", st);
-  return (int)cudaLaunchKernelEx(&cfg, weights_join_kernel, static_cast<const AwOpen*>(a.open),
-                                 static_cast<const float*>(a.part), a.weights, a.width, a.decay, (int)a.G, a.cu_k);
+  return launch_after(weights_join_kernel, dim3(ctas), kAwKeys, st, static_cast<const AwOpen*>(a.open), a.part,
+                      a.weights, a.width, a.decay, a.G, a.cu_k, a.errors, a.err);
 }
 
 }  // namespace msa

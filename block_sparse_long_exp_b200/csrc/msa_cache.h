@@ -93,13 +93,14 @@ struct AttnWeightsArgs {
   int32_t batch, H, G, d;
   const int32_t *cu_q, *cu_k;
   int64_t total_q, total_k;
-  DevError* err;
+  DevError* err;              // written by the join
   // workspace slices (attn_weights_layout)
+  DevError* errors;           // [CTA]
   void* open;                 // [CTA]: the key block that a CTA leaves to be joined
   float* part;                // [CTA, 2, 256]
 };
 struct AttnWeightsLayout {
-  size_t open, part, total;
+  size_t errors, open, part, total;
 };
 AttnWeightsLayout attn_weights_layout();
 int launch_attn_weights(const AttnWeightsArgs& a, void* stream);

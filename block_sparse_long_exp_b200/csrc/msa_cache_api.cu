@@ -77,14 +77,14 @@ msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16)) return MSA_ERR_INVALID_ARG;
   const AttnWeightsLayout L = attn_weights_layout();
   if (!ws_ok(ws, ws_bytes, L.total)) return MSA_ERR_WORKSPACE;
-  if (!clear_error(ws, stream)) return MSA_ERR_CUDA;
-  if (seqs->total_q == 0) return MSA_OK;
+  if (seqs->total_q == 0) return clear_error(ws, stream) ? MSA_OK : MSA_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(ws);
   AttnWeightsArgs a{};
   a.q = q; a.k = k; a.lse = lse; a.weights = weights; a.width = width; a.decay = decay;
   a.sm_scale = shape->sm_scale; a.batch = seqs->batch; a.H = shape->H; a.G = shape->G; a.d = shape->d;
   a.cu_q = seqs->cu_q; a.cu_k = seqs->cu_k; a.total_q = seqs->total_q; a.total_k = seqs->total_k;
   a.err = static_cast<DevError*>(ws);
+  a.errors = reinterpret_cast<DevError*>(base + L.errors);
   a.open = base + L.open;
   a.part = reinterpret_cast<float*>(base + L.part);
   return launch_attn_weights(a, stream) == 0 ? MSA_OK : MSA_ERR_CUDA;
