@@ -127,7 +127,7 @@ struct EvictMoveArgs {
   void *k, *v, *k_idx;        // pages, read and written
   const float* weights;       // [batch, G, src_blocks * 128] or null
   float* weights_out;         // [batch, G, dst_blocks * 128] or null
-  uint32_t* flags;            // [num_pages] of workspace, zeroed before the launch
+  uint32_t* flags;            // [num_pages] of workspace
   DevError* err;
 };
 int launch_evict_move(const EvictMoveArgs& a, void* stream);

@@ -135,9 +135,6 @@ msa_status_t msa_evict_move(const msa_shape_t* shape, const msa_paged_t* pages, 
   // the groups share the index keys: tokens kept by group have none of their own
   if (per_group != 0 && shape->G > 1 && k_idx_pages != nullptr) return MSA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, msa_evict_move_workspace_size(shape, pages))) return MSA_ERR_WORKSPACE;
-  if (cudaMemsetAsync(ws, 0, kWsHeader + sizeof(uint32_t) * (size_t)pages->num_pages,
-                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return MSA_ERR_CUDA;
   EvictMoveArgs a{};
   a.src_lens = pages->seqlens; a.src_table = pages->block_table;
   a.dst_lens = new_pages->seqlens; a.dst_table = new_pages->block_table;

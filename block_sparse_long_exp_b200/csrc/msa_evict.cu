@@ -558,10 +558,17 @@ struct MoveArgs {
 
 __device__ __forceinline__ int bounded_len(int L, int most) { return (L < 0 || L > most) ? 0 : L; }
 
+__global__ void __launch_bounds__(256) evict_clear_kernel(uint32_t* flags, int64_t n, DevError* err) {
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *err = DevError{0, 0, 0, 0};
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) flags[i] = 0u;
+}
+
 // Marks every page of the sources and counts every page of the destinations,
 // so that the move can tell a page that is both, or twice a destination.
 __global__ void __launch_bounds__(256) evict_mark_kernel(const MoveArgs a) {
   pdl_launch_dependents();                        // the move waits for this grid's end
+  pdl_wait();                                     // the flags are clear
   const int64_t src = (int64_t)a.batch * a.src_blocks, dst = (int64_t)a.batch * a.dst_blocks;
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < src + dst; i += gridDim.x * 256ll) {
     const bool from = i < src;
@@ -581,23 +588,16 @@ __global__ void __launch_bounds__(256) evict_mark_kernel(const MoveArgs a) {
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a, int chunks) {
   __shared__ int64_t src_row[4][kMoveRows];       // row of the pages; -1: nothing to copy
   __shared__ int32_t from[4][kMoveRows];          // position in the source; -1: none
-  pdl_wait();
   const int b = blockIdx.x / chunks, i0 = (blockIdx.x - b * chunks) * kMoveRows;
   const int tid = threadIdx.x;
   const int raw_src = a.src_lens[b], raw_dst = a.dst_lens[b];
   const int most = a.dst_max < a.kept_width ? a.dst_max : a.kept_width;
   const int L = bounded_len(raw_src, a.src_max), N = bounded_len(raw_dst, most);
-  if (i0 == 0 && tid == 0) {
-    if (L != raw_src) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, raw_src);
-    if (N != raw_dst) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, raw_dst);
-  }
   const int rows = min(kMoveRows, N - i0);
+  const int dst_blk = i0 / kBk;                   // dst_max is within dst_blocks pages
+  int page = -1, bad = -1;                        // the new page; a bad position's row or source block
   if (rows > 0) {
-    const int dst_blk = i0 / kBk;                 // dst_max is within dst_blocks pages
-    const int page = a.dst_table[(int64_t)b * a.dst_blocks + dst_blk];
-    bool page_ok = page >= 0 && page < a.num_pages;
-    if (page_ok) page_ok = a.flags[page] == 1u;   // a destination once, no source
-    if (!page_ok && tid == 0) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, dst_blk);
+    page = a.dst_table[(int64_t)b * a.dst_blocks + dst_blk];
     if (tid < a.R * kMoveRows) {
       const int r = tid / kMoveRows, x = tid - r * kMoveRows;
       int j = -1;
@@ -605,11 +605,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
       if (x < rows) {
         j = a.kept[((int64_t)b * a.R + r) * a.kept_width + i0 + x];
         if (j < 0 || j >= L) {
-          report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, i0 + x);
+          bad = i0 + x;
           j = -1;
         } else {
           const int p = a.src_table[(int64_t)b * a.src_blocks + j / kBk];
-          if (p < 0 || p >= a.num_pages) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, j / kBk);
+          if (p < 0 || p >= a.num_pages) bad = j / kBk;
           else row = gather_src_row(p, j % kBk, kBk);
         }
       }
@@ -617,30 +617,42 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
       src_row[r][x] = row;
     }
     __syncthreads();
+  }
+  pdl_wait();                                     // the pages are marked, and the error word is clear
+  if (i0 == 0 && tid == 0) {
+    if (L != raw_src) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, raw_src);
+    if (N != raw_dst) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, raw_dst);
+  }
+  if (rows > 0) {
+    if (bad >= 0) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, bad);
+    bool page_ok = page >= 0 && page < a.num_pages;
+    if (page_ok) page_ok = a.flags[page] == 1u;   // a destination once, no source
+    if (!page_ok && tid == 0) report_error(a.err, MSA_ERR_DEVICE_CHECK, kSiteEvictMove, b, dst_blk);
     if (page_ok) {
       const int64_t dst0 = gather_src_row(page, i0 % kBk, kBk);
+      // (four loads a thread in flight: 4 x 64K tokens in 191 us; with the streaming hints 193, and 218 with eight.)
       // words of a row, a power of two; with R == G a group's words come from its own token
       auto copy = [&](uint4* pages, int words, int pieces) {
         const int sh = 31 - __clz(words), psh = sh - (31 - __clz(pieces));
         const int n = rows << sh;
-        for (int w0 = tid; w0 < n; w0 += 8 * kMoveThreads) {
-          uint4 t[8];
-          bool have[8];
+        for (int w0 = tid; w0 < n; w0 += 4 * kMoveThreads) {
+          uint4 t[4];
+          bool have[4];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
+          for (int y = 0; y < 4; ++y) {
             const int w = w0 + y * kMoveThreads;
             have[y] = false;
             if (w < n) {
               const int x = w >> sh, col = w & (words - 1);
               const int64_t row = src_row[col >> psh][x];
               have[y] = row >= 0;
-              if (have[y]) t[y] = __ldcs(pages + (row << sh) + col);
+              if (have[y]) t[y] = pages[(row << sh) + col];
             }
           }
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
+          for (int y = 0; y < 4; ++y) {
             const int w = w0 + y * kMoveThreads;
-            if (have[y]) __stcs(pages + (dst0 << sh) + w, t[y]);
+            if (have[y]) pages[(dst0 << sh) + w] = t[y];
           }
         }
       };
@@ -751,28 +763,25 @@ int launch_evict_move(const EvictMoveArgs& m, void* stream) {
   a.k = static_cast<uint4*>(m.k); a.v = static_cast<uint4*>(m.v); a.k_idx = static_cast<uint4*>(m.k_idx);
   a.weights = m.weights; a.weights_out = m.weights_out; a.flags = m.flags; a.err = m.err;
   {
+    const int64_t want = (a.num_pages + 255) / 256;
+    prof_count_launch(1);
+    evict_clear_kernel<<<(unsigned)(want < 1184 ? want : 1184), 256, 0, st>>>(a.flags, a.num_pages, a.err);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return (int)e;
+  }
+  {
     const int64_t n = (int64_t)a.batch * ((int64_t)a.src_blocks + a.dst_blocks);
     const int64_t want = (n + 255) / 256;
     ProfScope p("evict_mark", stream);
-    evict_mark_kernel<<<(unsigned)(want < 1184 ? want : 1184), 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return (int)e;
+    const int rc = launch_after(evict_mark_kernel, dim3((unsigned)(want < 1184 ? want : 1184)), 256, st, a);
+    if (rc != 0) return rc;
   }
   // weights_out is written to its whole width, rows only up to the new lengths
   const int64_t last = a.weights_out != nullptr ? (int64_t)a.dst_blocks * kBk : a.dst_max;
   const int64_t chunks = (last + kMoveRows - 1) / kMoveRows;
   if (chunks * a.batch > 0x7fffffffLL) return (int)cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(chunks * a.batch));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   ProfScope p("evict_move", stream);
-  return (int)cudaLaunchKernelEx(&cfg, evict_move_kernel, a, (int)chunks);
+  return launch_after(evict_move_kernel, dim3((unsigned)(chunks * a.batch)), kMoveThreads, st, a, (int)chunks);
 }
 
 }  // namespace msa
