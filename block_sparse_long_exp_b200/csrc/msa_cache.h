@@ -115,7 +115,7 @@ struct EvictSelectArgs {
   void* work;                 // evict_select_work_bytes of workspace, right behind the header of err
   DevError* err;              // written in any case
 };
-// Workspace behind the header (0 where one CTA has a sequence's keys).
+// Workspace behind the header (0 where registers hold a sequence's keys).
 size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen);
 int launch_evict_select(const EvictSelectArgs& a, void* stream);
 

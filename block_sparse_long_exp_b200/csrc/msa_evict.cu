@@ -7,22 +7,24 @@
 //   key T is found by its bits: 11, 11 and 10 at a time, a histogram of the keys
 //   that share the bits found so far.  Kept: the keys above T and, of those
 //   equal to T, the first ones.  Counts are whole numbers, so the result does
-//   not depend on the order of the atomics.  Up to 8192 tokens one CTA has a
-//   (sequence, ranking), the keys in its registers and the histograms in shared
-//   memory, and what it takes is the latency of some fifteen barriers; beyond,
-//   a CTA has 4096 tokens and the steps are launches.  Bound by those launches
-//   up to some 300,000 tokens in all, then by the weights from HBM.
+//   not depend on the order of the atomics.  Up to 65,536 tokens a CTA, or a
+//   cluster of them that add up their histograms from one another's shared
+//   memory, has a (sequence, ranking), the keys in registers, and what it takes is
+//   the latency of some fifteen barriers; beyond, a CTA has 4096 tokens and the
+//   steps are launches.  Bound by those launches up to some 300,000 tokens in
+//   all, then by the weights from HBM.
 // move: the rows of the kept tokens gathered into other pages; reads and writes
 //   each kept byte once (HBM).  Out of place: a page of the source may be shared
 //   with another sequence, and the rows can go in any order.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
-
-#include <atomic>
 
 #include "msa_common.cuh"
 #include "msa_cache.h"
 #include "msa_gather.h"
 #include "msa_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace msa {
 namespace {
@@ -174,26 +176,32 @@ __device__ __forceinline__ int find_lane(uint32_t c, uint32_t need, uint32_t* ab
 
 struct SelCtl {
   union {
-    uint32_t hist[3][2048];
-    int32_t list[kSelPart];   // afterwards: the kept tokens in their order
+    struct {
+      uint32_t hist[3][2048];
+      uint32_t sum[2048];     // a cluster's histogram
+    };
+    int32_t list[kSelPart];   // afterwards: the CTA's kept tokens in their order
   };
   uint32_t warp_sum[kSelWarps];
+  uint32_t gt, eq;            // this CTA's keys above and equal to the threshold
 };
 
-// A CTA per (sequence, ranking).
-template <int GS, int PER>
+// A CTA, or a cluster of them, per (sequence, ranking).
+template <bool kCluster, int GS, int PER>
 __global__ void __launch_bounds__(kSelThreads, 1)
 evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, const int32_t* __restrict__ seqlens,
                     int batch, int max_seqlen, int budget, int n_sink, int n_recent, int32_t* __restrict__ kept,
                     int32_t* __restrict__ new_lens, DevError* err) {
   __shared__ SelCtl ctl;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = kCluster ? cluster.num_blocks() : 1, rank = kCluster ? cluster.block_rank() : 0;
   const int R = GS == 1 ? G : 1;
-  const int row = blockIdx.x, b = row / R, r = row - b * R;
+  const int row = blockIdx.x / cs, b = row / R, r = row - b * R;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bounded = [&](int n) { return n < 0 || n > max_seqlen ? 0 : n; };
   const int L = bounded(seqlens[b]);
   int32_t* dst = kept + (int64_t)row * budget;
-  if (tid == 0 && r == 0) new_lens[b] = L < budget ? L : budget;
+  if (rank == 0 && tid == 0 && r == 0) new_lens[b] = L < budget ? L : budget;
   if (blockIdx.x == 0) {                          // the first bad length, or none
     int bad = batch;
     for (int i = tid; i < batch; i += kSelThreads)
@@ -208,22 +216,24 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
     }
     __syncthreads();
   }
-  if (L <= budget) {                              // every token stays
-    for (int64_t i = tid; i < budget; i += kSelThreads) dst[i] = i < L ? (int32_t)i : -1;
+  if (L <= budget) {                              // every token stays (the whole cluster takes this way)
+    for (int64_t i = rank * kSelThreads + tid; i < budget; i += cs * kSelThreads) dst[i] = i < L ? (int32_t)i : -1;
     return;
   }
 
-  // ---- PER tokens in a row to a thread
+  // ---- this CTA's tokens [j0, j0 + n), PER in a row to a thread
+  const int per = ((L + cs - 1) / cs + PER - 1) / PER * PER;
+  const int j0 = min(rank * per, L), n = min(per, L - j0);
   const int i0 = tid * PER;
   uint32_t key[PER];
 #pragma unroll
   for (int x = 0; x < PER; ++x) key[x] = 0u;
-  if (i0 < L) token_scores<GS>(weights + ((int64_t)b * G + r) * width + i0, width, key);   // rows reach past L to their width
+  if (i0 < n) token_scores<GS>(weights + ((int64_t)b * G + r) * width + j0 + i0, width, key);   // rows reach past L to their width
   for (int i = tid; i < 3 * 2048; i += kSelThreads) (&ctl.hist[0][0])[i] = 0u;
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    const int j = i0 + x;
+    const int j = j0 + i0 + x;
     key[x] = (j < n_sink || j >= L - n_recent) ? kForced : order_key(key[x]);
   }
 
@@ -238,12 +248,24 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
       bins[x] = key[x] >> kDown[pass] & (pass == 2 ? 1023u : 2047u);
-      in[x] = i0 + x < L && (pass == 0 || key[x] >> kShift[pass] == top);
+      in[x] = i0 + x < n && (pass == 0 || key[x] >> kShift[pass] == top);
     }
     count_bins(hist, bins, in);
     // a thread has two bins; every warp finds the bin from the warps' sums
-    __syncthreads();
-    const uint2 c = reinterpret_cast<const uint2*>(hist)[tid];
+    uint2 c = make_uint2(0u, 0u);
+    if constexpr (kCluster) {
+      cluster.sync();
+      for (int k = 0; k < cs; ++k) {
+        const uint2 v = reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, k))[tid];
+        c.x += v.x;
+        c.y += v.y;
+      }
+      reinterpret_cast<uint2*>(ctl.sum)[tid] = c;
+      hist = ctl.sum;
+    } else {
+      __syncthreads();
+      c = reinterpret_cast<const uint2*>(hist)[tid];
+    }
     const uint32_t w = __reduce_add_sync(0xffffffffu, c.x + c.y);
     if (lane == 0) ctl.warp_sum[warp] = w;
     __syncthreads();
@@ -262,25 +284,42 @@ evict_select_kernel(const float* __restrict__ weights, int G, int64_t width, con
   uint32_t f = 0;                                 // above | equal << 16 of the thread's tokens
 #pragma unroll
   for (int x = 0; x < PER; ++x)
-    if (i0 + x < L) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
+    if (i0 + x < n) f += key[x] > top ? 1u : (key[x] == top ? 0x10000u : 0u);
   uint32_t total;
   const uint32_t before = block_scan<kSelWarps>(f, ctl.warp_sum, &total);
+  uint32_t eq0 = 0, first = 0;                    // equal keys of the CTAs before this one; kept tokens of theirs
+  if constexpr (kCluster) {
+    if (tid == 0) {
+      ctl.gt = total & 0xffffu;
+      ctl.eq = total >> 16;
+    }
+    cluster.sync();                               // (and every histogram is read)
+    for (int k = 0; k < rank; ++k) {
+      const SelCtl* other = cluster.map_shared_rank(&ctl, k);
+      first += other->gt;
+      eq0 += other->eq;
+    }
+    first += min(eq0, need);
+  }
+  const uint32_t left = need - min(eq0, need);    // equal keys that this CTA may keep
   // the list is put in order in shared memory (every histogram is read) and goes out in whole lines
   uint32_t gt = before & 0xffffu, eq = before >> 16;
 #pragma unroll
   for (int x = 0; x < PER; ++x) {
-    if (i0 + x < L) {
+    if (i0 + x < n) {
       if (key[x] > top) {
-        ctl.list[gt + min(eq, need)] = i0 + x;
+        ctl.list[gt + min(eq, left)] = j0 + i0 + x;
         ++gt;
       } else if (key[x] == top) {
-        if (eq < need) ctl.list[gt + eq] = i0 + x;
+        if (eq < left) ctl.list[gt + eq] = j0 + i0 + x;
         ++eq;
       }
     }
   }
   __syncthreads();
-  for (int i = tid; i < budget; i += kSelThreads) dst[i] = ctl.list[i];
+  const int here = (int)((total & 0xffffu) + min(total >> 16, left));
+  for (int i = tid; i < here; i += kSelThreads) dst[first + i] = ctl.list[i];
+  if constexpr (kCluster) cluster.sync();         // the others read this CTA's counts
 }
 
 // -------------------------------------------------- select, long sequences ---
@@ -675,11 +714,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   }
 }
 
-// Beyond one CTA's tokens a (sequence, ranking) has a CTA per 4096 and six
-// launches: 13.6 us for 10K to 200K tokens, where a cluster of CTAs with the
-// histograms in shared memory took 13.2 for 10K, 14.8 for 20K and 20.4 for 40K;
-// one CTA takes 8.9 us for 5K.
-constexpr int32_t kLongFrom = kSelPart;
+// One launch, with a cluster of up to eight CTAs per (sequence, ranking), or six
+// with a CTA per 4096 tokens?  In a graph 10K tokens take 13.2 us and 13.6, 40K
+// 18.1 and 14.0; called one by one from Python 14.4 us and 26.6, 20.2 and 26.6.
+// More clusters than run at once lose both ways (16 x 40K: 35 us and 19).
+constexpr int kMaxCluster = 8, kMostCtas = 96;
+int cluster_of(int32_t max_seqlen) {
+  int cs = 1;
+  while (cs <= kMaxCluster && max_seqlen > cs * kSelPart) cs *= 2;
+  return cs;
+}
+bool by_launches(int64_t rows, int32_t max_seqlen) {
+  const int cs = cluster_of(max_seqlen);
+  return cs > kMaxCluster || (cs > 1 && rows * cs > kMostCtas);
+}
 
 struct LongLayout {
   int32_t parts;
@@ -736,20 +784,35 @@ int launch_long_select(const EvictSelectArgs& s, cudaStream_t st) {
 }  // namespace
 
 size_t evict_select_work_bytes(int32_t batch, int32_t rankings, int32_t max_seqlen) {
-  return max_seqlen > kLongFrom ? long_layout((int64_t)batch * rankings, max_seqlen).total : 0;
+  const int64_t rows = (int64_t)batch * rankings;
+  return by_launches(rows, max_seqlen) ? long_layout(rows, max_seqlen).total : 0;
 }
 
 int launch_evict_select(const EvictSelectArgs& a, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (a.max_seqlen > kLongFrom) return launch_long_select(a, st);
+  const int64_t rows = (int64_t)a.batch * (a.per_group ? a.G : 1);
+  if (by_launches(rows, a.max_seqlen)) return launch_long_select(a, st);
   const int gs = a.per_group ? 1 : a.G;
-#define MSA_SELECT(P) (gs == 1 ? evict_select_kernel<1, P> : gs == 2 ? evict_select_kernel<2, P> : evict_select_kernel<4, P>)
-  auto* kernel = a.max_seqlen > 4 * kSelThreads ? MSA_SELECT(8) : MSA_SELECT(4);   // 1K tokens: 6.2 us with 4, 8.7 with 8
+  const int cs = cluster_of(a.max_seqlen);
+  // 1K tokens: 5.8 us with four tokens a thread, 8.7 with eight
+#define MSA_SELECT(C, P) \
+  (gs == 1 ? evict_select_kernel<C, 1, P> : gs == 2 ? evict_select_kernel<C, 2, P> : evict_select_kernel<C, 4, P>)
+  auto* kernel = cs > 1 ? MSA_SELECT(true, 8) : a.max_seqlen > 4 * kSelThreads ? MSA_SELECT(false, 8) : MSA_SELECT(false, 4);
 #undef MSA_SELECT
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * cs));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
   ProfScope p("evict_select", stream);
-  kernel<<<(unsigned)(a.batch * (a.per_group ? a.G : 1)), kSelThreads, 0, st>>>(
-      a.weights, a.G, a.width, a.seqlens, a.batch, a.max_seqlen, a.budget, a.n_sink, a.n_recent, a.kept, a.new_lens, a.err);
-  return (int)cudaGetLastError();
+  return (int)cudaLaunchKernelEx(&cfg, kernel, a.weights, a.G, a.width, a.seqlens, a.batch, a.max_seqlen, a.budget,
+                                 a.n_sink, a.n_recent, a.kept, a.new_lens, a.err);
 }
 
 int launch_evict_move(const EvictMoveArgs& m, void* stream) {

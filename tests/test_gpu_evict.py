@@ -122,6 +122,18 @@ def test_keys_past_shared_memory(M, lens):
         assert new.cpu().tolist() == [min(n, budget) for n in lens]
 
 
+@pytest.mark.parametrize("L,B", [(9001, 1), (9001, 40), (20000, 3), (20000, 25), (33000, 2), (33000, 13)])
+def test_clusters_and_launches(M, L, B):
+    # few rankings: a cluster of CTAs each; many: a CTA per part of each
+    lens = [max(1, L - 997 * b) for b in range(B)]
+    blocks = -(-L // PAGE)
+    for kind, budget in (("spread", L // 5), ("ties", L // 2)):
+        w = _weights(B, 2, blocks, B, kind)
+        kept, new = M.msa_evict_select(M.make_shape(8, 2, 64, 64, 16), _pages(M, lens, blocks=blocks), w.cuda(), budget, 3, 40)
+        assert torch.equal(kept[:, 0].cpu(), _want_fast(w, lens, budget, 3, 40))
+        assert new.cpu().tolist() == [min(n, budget) for n in lens]
+
+
 @pytest.mark.parametrize("per_group", [False, True])
 def test_long_and_short_in_one_batch(M, per_group):
     # the longest decides the launch: rows that keep all, empty ones and bad lengths beside it
