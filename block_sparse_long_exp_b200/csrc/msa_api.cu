@@ -8,6 +8,7 @@
 #include <climits>
 #include <mutex>
 
+#include "msa_cache.h"
 #include "msa_internal.h"
 #include "msa_kl.h"
 #include "msa_window.h"

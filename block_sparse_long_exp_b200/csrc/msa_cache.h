@@ -11,9 +11,14 @@
 
 #include <cuda_runtime.h>
 
+#include "../../include/msa.h"
+
 namespace msa {
 
 struct DevError;
+
+// Host-side check of a paged description (msa_api.cu).
+msa_status_t check_paged(const msa_shape_t* s, const msa_paged_t* pg);
 
 // DevError::where of these kernels.
 constexpr int32_t kSiteDenseDecode = 241;   // lengths, pages and waits of the dense paged decode

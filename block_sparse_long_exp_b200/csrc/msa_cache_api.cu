@@ -16,6 +16,9 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool ws_ok(const void* ws, size_t have, size_t need) { return ws != nullptr && aligned(ws, 256) && have >= need; }
 
+// Keys past a sequence's end count as scores of -inf, which a scale of 0 or below would turn into something else.
+bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
+
 bool decay_ok(float d) { return d >= 0.f && d <= 1.f; }
 
 bool clear_error(void* ws, void* stream) {
@@ -40,7 +43,7 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
   if (!q || !k_pages || !v_pages || !out) return MSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
     return MSA_ERR_INVALID_ARG;
-  if (weights != nullptr && !decay_ok(decay)) return MSA_ERR_INVALID_ARG;
+  if (!scale_ok(shape->sm_scale) || (weights != nullptr && !decay_ok(decay))) return MSA_ERR_INVALID_ARG;
   const DenseDecodeLayout L =
       dense_decode_layout(pages->batch, shape->H, shape->d, pages->max_seqlen, weights != nullptr);
   if (!ws_ok(ws, ws_bytes, L.total)) return MSA_ERR_WORKSPACE;
@@ -72,7 +75,7 @@ msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs
   if (st != MSA_OK) return st;
   st = check_seqs(seqs);
   if (st != MSA_OK) return st;
-  if (width < seqs->max_k_len || !decay_ok(decay)) return MSA_ERR_INVALID_ARG;
+  if (width < seqs->max_k_len || !scale_ok(shape->sm_scale) || !decay_ok(decay)) return MSA_ERR_INVALID_ARG;
   if (seqs->total_q > 0 && (!q || !k || !lse || !weights)) return MSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16)) return MSA_ERR_INVALID_ARG;
   const AttnWeightsLayout L = attn_weights_layout();

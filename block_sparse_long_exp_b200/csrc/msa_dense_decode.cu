@@ -68,6 +68,20 @@ struct DecCtl {
   float ml[4][2][16];           // (m, l) rows of the merging warps
 };
 
+// A tensor load of data that is read once: its lines leave L2 first.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -815,7 +829,7 @@ int launch_dense_decode(const DenseDecodeArgs& a, void* stream) {
   {
     ProfScope p("dense_join", stream);
     // few sequences lie in many runs each: eight warps to a (b, h), and up to two sequences its columns over 2 or 4
-    // CTAs (1 x 1M tokens: JOINWIDE us against JOINMID); many lie in few: one warp
+    // CTAs; many lie in few: one warp
 #define MSA_JOIN(DD, W, VEC)                                                                                       \
   rc = launch_after(dense_join_kernel<DD, W, VEC>,                                                                 \
                     dim3((unsigned)((pairs + 8 / W - 1) / (8 / W) * (DD / (32 * VEC)))), 256, st, out, a.lse, a.batch,     \

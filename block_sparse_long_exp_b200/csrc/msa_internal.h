@@ -70,7 +70,6 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 msa_status_t check_shape(const msa_shape_t* s);
 msa_status_t check_shape_bk128(const msa_shape_t* s);
 msa_status_t check_seqs(const msa_varlen_t* v);
-msa_status_t check_paged(const msa_shape_t* s, const msa_paged_t* pg);
 
 // -------------------------------------------------------- host launchers ---
 // Each returns the cudaError_t of its launch(es) (0 on success).

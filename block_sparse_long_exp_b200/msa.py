@@ -1062,13 +1062,16 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
     (entries past a sequence's end stay).  A length of 0 is a padded row: out 0,
     lse -inf."""
     lib = load_library()
-    B, rows = pages.batch, pages.num_pages * 128
-    _arg("q", q, torch.bfloat16, (B, shape.H, shape.d))
-    _arg("k_pages", k_pages, torch.bfloat16, (rows, shape.G, shape.d))
-    _arg("v_pages", v_pages, torch.bfloat16, (rows, shape.G, shape.d))
-    _arg("out", out, torch.bfloat16, (B, shape.H, shape.d), optional=True)
-    _arg("lse", lse, torch.float32, (B, shape.H), optional=True)
-    _arg("weights", weights, torch.float32, (B, shape.G, pages.max_blocks * 128), optional=True)
+    B, rows, H, G, d = pages.batch, pages.num_pages * 128, shape.H, shape.G, shape.d
+    _arg("q", q, torch.bfloat16, (B, H, d))
+    _arg("k_pages", k_pages, torch.bfloat16, (rows, G, d))
+    _arg("v_pages", v_pages, torch.bfloat16, (rows, G, d))
+    if out is not None:
+        _arg("out", out, torch.bfloat16, (B, H, d))
+    if lse is not None:
+        _arg("lse", lse, torch.float32, (B, H))
+    if weights is not None:
+        _arg("weights", weights, torch.float32, (B, G, pages.max_blocks * 128))
     decay = _decay(decay)
     _ws_arg(ws)
     _require_cuda(q, k_pages, v_pages, out, lse, weights, ws, *getattr(pages, "_keep", ()))
@@ -1076,7 +1079,7 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
-            lse = q.new_empty((B, shape.H), dtype=torch.float32)
+            lse = q.new_empty((B, H), dtype=torch.float32)
         if ws is None:
             need = msa_dense_attn_decode_paged_workspace_size(shape, pages, weights is not None)
             if need == 0:

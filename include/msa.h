@@ -469,8 +469,8 @@ msa_status_t msa_dense_attn(const msa_shape_t* shape, const msa_varlen_t* seqs,
  * too, and its tokens are left out (nothing is read out of range).  Rows of a
  * page past the sequence's end may hold anything.  A head whose scores are all
  * -inf gets out 0 and lse -inf.
- * q, k_pages, v_pages and out 16-byte aligned, else MSA_ERR_INVALID_ARG.  The
- * parts of a sequence are joined in a fixed order: results are the same from
+ * q, k_pages, v_pages and out 16-byte aligned, sm_scale positive and finite, else
+ * MSA_ERR_INVALID_ARG.  The parts of a sequence are joined in a fixed order: results are the same from
  * run to run (on one device model).  Workspace: with_weights != 0 adds 4 H
  * bytes per sequence and token of max_seqlen (the scores, in 32 bits). */
 size_t msa_dense_attn_decode_paged_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages,
@@ -497,7 +497,7 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
  * are not touched, nor is a sequence without queries.  A (query, head) whose lse
  * is -inf has seen no key and adds nothing.  width >= max_k_len (a paged cache's
  * max_blocks * 128, so that decode steps go on from it), q, k and lse 16-byte
- * aligned, else MSA_ERR_INVALID_ARG.  A sequence with more queries than keys is
+ * aligned, sm_scale positive and finite, else MSA_ERR_INVALID_ARG.  A sequence with more queries than keys is
  * recorded as MSA_ERR_DEVICE_CHECK and left as it is.  Sums are 32-bit and in a
  * fixed order: the same from run to run (on one device model). */
 size_t msa_attn_weights_workspace_size(const msa_shape_t* shape, const msa_varlen_t* seqs);

@@ -59,6 +59,8 @@ def test_dense_decode_host_checks(M):
     no_table = _pages(M)
     no_table.block_table = None
     assert call(pg=no_table) == INVALID
+    for scale in (0.0, -0.1, float("inf"), float("nan")):
+        assert call(shape=M.make_shape(64, 4, 128, 64, 16, sm_scale=scale)) == INVALID
 
 
 def test_attn_weights_host_checks(M):
@@ -75,6 +77,8 @@ def test_attn_weights_host_checks(M):
                   {"width": 299}, {"width": 0}, {"decay": -1.0}, {"decay": 2.0}, {"decay": float("nan")},
                   {"seqs": M.Varlen(1, 301, 300, 0, 301, 300, A, A)}, {"seqs": M.Varlen(0, 64, 300, 0, 64, 300, A, A)}):
         assert call(**wrong) == INVALID, wrong
+    for scale in (0.0, -0.1, float("inf"), float("nan")):
+        assert call(shape=M.make_shape(64, 4, 128, 64, 16, sm_scale=scale)) == INVALID
     assert call(n=255) == WORKSPACE and call(ws=A + 128) == WORKSPACE
     assert call(shape=M.make_shape(64, 4, 80, 64, 16)) == UNSUPPORTED
 
