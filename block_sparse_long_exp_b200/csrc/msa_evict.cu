@@ -12,10 +12,12 @@
 //   memory, has a (sequence, ranking), the keys in registers, and what it takes is
 //   the latency of some fifteen barriers; beyond, a CTA has 4096 tokens and the
 //   steps are launches.  Bound by those launches up to some 300,000 tokens in
-//   all, then by the weights from HBM.
+//   all, then by the weights from HBM.  On a B200: 8 x 5K tokens 8.9 us in a
+//   graph (14.1 called one by one), 2 x 1M 33.6 us.
 // move: the rows of the kept tokens gathered into other pages; reads and writes
 //   each kept byte once (HBM).  Out of place: a page of the source may be shared
-//   with another sequence, and the rows can go in any order.
+//   with another sequence, and the rows can go in any order.  On a B200: 4 x 64K
+//   rows (G 4, d 128) 188 us, 6.1 TB/s; 8 x 4K by group 29.3 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
