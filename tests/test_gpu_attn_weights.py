@@ -345,3 +345,41 @@ def test_prompt_decode_and_eviction_in_a_row(M, per_group):
         assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -12 * mass)
         assert torch.allclose(w2[b, :, :nl[b]].double().cpu(), before[b, :, :nl[b]] * decay + torch.from_numpy(ww),
                               rtol=2.0 ** -11, atol=0)
+
+
+def test_workspace_with_anything_in_it_and_other_scales(M):
+    T, S = [300, 0, 64], [300, 9, 900]
+    H, G, d = 16, 2, 128
+    q, k = _inputs(H, G, d, T, S, 151)
+    seqs = _varlen(M, T, S)
+    for scale in (1e-3, 0.7):
+        shape = M.make_shape(H, G, d, 64, 16, sm_scale=scale)
+        lse = _lse(q, k, T, S, scale)
+        ws = torch.full((M.msa_attn_weights_workspace_size(shape, seqs),), 255, dtype=torch.uint8, device="cuda")
+        w0 = torch.rand(3, G, 900)
+        w = w0.cuda()
+        M.msa_attn_weights(shape, seqs, q.cuda(), k.cuda(), lse.cuda(), weights=w, decay=0.3, ws=ws)
+        _check(w.cpu(), q, k, lse, T, S, scale, w0, 0.3)
+
+
+def test_exponentials_far_from_zero(M):
+    # one score per query and a log-sum-exp of its own: exp(s - lse) from 2^-140 (0 in 32 bits) to 2^120
+    H, G, d, T = 4, 1, 64, 400
+    shape = M.make_shape(H, G, d, 64, 16)
+    q, k = torch.zeros(T, H, d).bfloat16(), torch.zeros(T, G, d).bfloat16()
+    x = torch.linspace(-140, 120, T)
+    lse = (-x * np.log(2.0))[:, None].expand(T, H).contiguous()
+    w = M.msa_attn_weights(shape, _varlen(M, [T], [T]), q.cuda(), k.cuda(), lse.cuda()).cpu().double()[0, 0]
+    terms = H * torch.exp(-lse[:, 0].double())
+    want = torch.flip(torch.cumsum(torch.flip(terms, [0]), 0), [0])          # key j is seen by the queries from j on
+    # arguments of up to 140: two roundings and the difference are off by 140 x 3 x 2^-24 of the exponent, 2^-16 for the rest
+    assert bool(((w - want).abs() <= want * (np.log(2.0) * 140 * 3 * 2.0 ** -24 + 2.0 ** -16)).all())
+    # a query alone, from each end of the range: tiny results flush to 0, none comes out wrong
+    for e in (-149.0, -130.0, -127.5, -127.0, -126.5, -126.0, -1.0, 0.0, 1.0, 100.0, 126.0):
+        one = M.msa_attn_weights(shape, _varlen(M, [1], [1]), q[:1].cuda(), k[:1].cuda(),
+                                 torch.full((1, H), float(-e * np.log(2.0)), dtype=torch.float32).cuda()).item()
+        exact = H * 2.0 ** e
+        if exact >= 2.0 ** 128:                                   # 4 x 2^126 is past the largest 32-bit number, 2^128 - 2^104
+            assert one == float("inf")
+            continue
+        assert abs(one - exact) <= exact * 2.0 ** -14 + H * 2.0 ** -126, (e, one)

@@ -292,3 +292,53 @@ def test_offsets_past_32_bits(M):
     for b, n in enumerate(lens):
         head[b, :, n:] = 0
     _check(out.cpu(), lse.cpu(), head, q, seqs, shape.sm_scale, w0)
+
+
+def test_more_rows_than_a_grid_dimension_holds(M):
+    # 66000 padded or one-page rows over the same few pages
+    H, G, d, B = 4, 1, 64, 66000
+    k, v, table, pages, seqs = _paged([128, 128], G, d, 141)
+    lens = torch.zeros(B, dtype=torch.int32)
+    at = {0: 128, 1: 1, 77: 17, 65534: 100, 65535: 64, 65536: 65, 65999: 128}
+    for b, n in at.items():
+        lens[b] = n
+    tab = table[torch.arange(B) % 2][:, :1].contiguous()
+    q = torch.randn(B, H, d, generator=torch.Generator().manual_seed(5)).bfloat16()
+    shape = M.make_shape(H, G, d, 64, 16)
+    pg = M.make_paged(lens.cuda(), tab.cuda(), 128, pages)
+    w0 = torch.rand(B, G, PAGE, generator=torch.Generator().manual_seed(6))
+    w = w0.cuda()
+    out, lse = M.msa_dense_attn_decode_paged(shape, pg, q.cuda(), k.cuda(), v.cuda(), weights=w, decay=0.5)
+    out, lse, w = out.cpu(), lse.cpu(), w.cpu()
+    rows = sorted(at)
+    part = [(seqs[b % 2][0][:at[b]], seqs[b % 2][1][:at[b]]) for b in rows]
+    _check(out[rows], lse[rows], w[rows], q[rows], part, shape.sm_scale, w0[rows], 0.5)
+    empty = torch.ones(B, dtype=torch.bool)
+    empty[rows] = False
+    assert torch.all(out[empty] == 0) and torch.all(lse[empty] == float("-inf")) and torch.equal(w[empty], w0[empty])
+
+
+@pytest.mark.parametrize("scale", [1e-3, 2.0])
+def test_other_scales(M, scale):
+    H, G, d, lens = 16, 2, 64, [300, 70]
+    k, v, table, pages, seqs = _paged(lens, G, d, 151)
+    q = torch.randn(2, H, d, generator=torch.Generator().manual_seed(7)).bfloat16()
+    shape = M.make_shape(H, G, d, 64, 16, sm_scale=scale)
+    pg = M.make_paged(torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(), 300, pages)
+    w0 = torch.zeros(2, G, table.shape[1] * PAGE)
+    w = w0.cuda()
+    out, lse = M.msa_dense_attn_decode_paged(shape, pg, q.cuda(), k.cuda(), v.cuda(), weights=w)
+    _check(out.cpu(), lse.cpu(), w.cpu(), q, seqs, scale, w0)
+
+
+def test_workspace_with_anything_in_it(M):
+    lens = [500, 0, 9000]
+    k, v, table, pages, seqs = _paged(lens, 2, 128, 161)
+    q = torch.randn(3, 32, 128, generator=torch.Generator().manual_seed(8)).bfloat16()
+    shape = M.make_shape(32, 2, 128, 64, 16)
+    pg = M.make_paged(torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(), 9000, pages)
+    ws = torch.full((M.msa_dense_attn_decode_paged_workspace_size(shape, pg, True),), 255, dtype=torch.uint8, device="cuda")
+    w0 = torch.zeros(3, 2, table.shape[1] * PAGE)
+    w = w0.cuda()
+    out, lse = M.msa_dense_attn_decode_paged(shape, pg, q.cuda(), k.cuda(), v.cuda(), weights=w, ws=ws)
+    _check(out.cpu(), lse.cpu(), w.cpu(), q, seqs, shape.sm_scale, w0)

@@ -379,3 +379,60 @@ def test_pool_past_4_gib(M):
         r = _row(new_table, 0, i)
         want = torch.stack([rows[int(kc[0, gg, i]), gg] for gg in range(G)])
         assert torch.equal(big[0][r].cpu(), want) and torch.equal(big[1][r].cpu(), -want)
+
+
+@pytest.mark.parametrize("L", [300, 20000, 70000])
+def test_workspaces_with_anything_in_them(M, L):
+    blocks = -(-L // PAGE)
+    w = _weights(2, 2, blocks, 23)
+    lens = [L, L - 50]
+    shape = M.make_shape(8, 2, 64, 32, 16)
+    pg = _pages(M, lens, blocks=blocks)
+    ws = torch.full((M.msa_evict_select_workspace_size(shape, pg),), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        kept, new = M.msa_evict_select(shape, pg, w.cuda(), L // 2, 3, 40, ws=ws)
+        assert torch.equal(kept[:, 0].cpu(), _want_fast(w, lens, L // 2, 3, 40)) and new.cpu().tolist() == [L // 2] * 2
+    pool = _pool(2, 64, 32, 2 * blocks + 4, 24)
+    spg = M.make_paged(torch.tensor(lens, dtype=torch.int32).cuda(),
+                       torch.arange(2 * blocks, dtype=torch.int32).view(2, blocks).cuda(), L, 2 * blocks + 4)
+    kept, new = M.msa_evict_select(shape, spg, w.cuda(), 200, 3, 40)
+    new_table = 2 * blocks + torch.arange(4, dtype=torch.int32).view(2, 2)
+    ws = torch.full((M.msa_evict_move_workspace_size(shape, spg),), 255, dtype=torch.uint8, device="cuda")
+    dev = [x.cuda() for x in pool]
+    out = M.msa_evict_move(shape, spg, M.make_paged(new, new_table.cuda(), 200, 2 * blocks + 4), kept, dev[0], dev[1],
+                           k_idx_pages=dev[2], weights=w.cuda(), ws=ws)
+    k, v, ki, want = _moved(pool, spg._keep[1].cpu(), new_table, kept.cpu(), [200, 200], w, 256)
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(dev, (k, v, ki))) and torch.equal(out.cpu(), want)
+
+
+def test_many_rows(M):
+    B = 66000
+    lens = [200 if b % 1000 == 7 else (b % 3) for b in range(B)]
+    w = _weights(1, 1, 2, 25).expand(B, 1, 256).contiguous()
+    pg = M.make_paged(torch.tensor(lens, dtype=torch.int32).cuda(), torch.zeros(B, 2, dtype=torch.int32).cuda(), 200, 1)
+    kept, new = M.msa_evict_select(M.make_shape(4, 1, 64, 64, 16), pg, w.cuda(), 60, 1, 9)
+    want = {n: torch.from_numpy(_want(w[:1], [n], 60, 1, 9, False))[0] for n in (0, 1, 2, 200)}
+    assert torch.equal(kept.cpu(), torch.stack([want[n] for n in lens]))
+    assert new.cpu().tolist() == [min(n, 60) for n in lens]
+
+
+@pytest.mark.parametrize("L", [20000, 70000])
+def test_choice_in_a_graph(M, L):
+    blocks = -(-L // PAGE)
+    shape = M.make_shape(8, 2, 64, 64, 16)
+    lens_d = torch.tensor([L, L], dtype=torch.int32).cuda()
+    pg = M.make_paged(lens_d, torch.zeros(2, blocks, dtype=torch.int32).cuda(), L, 1)
+    wd = torch.empty(2, 2, blocks * PAGE, device="cuda")
+    kept, new = torch.empty(2, 1, 900, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(M.msa_evict_select_workspace_size(shape, pg), dtype=torch.uint8, device="cuda")
+    wd.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.msa_evict_select(shape, pg, wd, 900, 3, 40, kept=kept, new_lens=new, ws=ws, check=False)
+    for i, lens in enumerate(([L, L - 9], [901, L], [L, 20])):
+        w = _weights(2, 2, blocks, 30 + i, "ties" if i == 1 else "spread")
+        wd.copy_(w)
+        lens_d.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept[:, 0].cpu(), _want_fast(w, lens, 900, 3, 40)) and new.cpu().tolist() == [min(n, 900) for n in lens]
