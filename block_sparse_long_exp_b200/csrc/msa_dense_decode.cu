@@ -4,9 +4,10 @@
 //
 // For head h of group g and the keys j < L of its sequence
 //   s_j = <q_h, k_j>,  out_h = sum_j e_j v_j / l,  e_j = 2^(c s_j - m),  l = sum_j e_j,
-// with c = sm_scale log2(e) and m the largest c s_j so far, as a 32-bit number
-// (a new maximum rescales the sums by 2^(m_old - m_new), exact in m).  Parts of
-// the keys have (m, l, o) of their own and join by the same rescaling.
+// with c = sm_scale log2(e) and m a 32-bit number no more than 8 below the largest
+// c s_j so far (a larger one takes its place and rescales the sums by 2^(m_old -
+// m_new), exact in m; letting e_j reach 2^8 spares most of that).  Parts of the keys
+// have (m, l, o) of their own and join by the same rescaling.
 //
 // The step is bound by HBM: every cached key and value is read once and meets
 // H / G query heads, 16 operations a byte at most.  On a B200 (H 64, G 4, d 128):
@@ -48,6 +49,7 @@ constexpr int kSets = 2;                          // tiles in work at once
 constexpr int kComputeWarps = 4 * kSets;
 constexpr int kDecThreads = 32 * (kComputeWarps + 1);
 constexpr int kTileTok = 16;                      // tokens of a warp in a tile
+constexpr float kSlack = 8.f;                     // how far above m a score may be, in units of log2
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -103,6 +105,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void compute_bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
@@ -323,9 +330,8 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (; t < e; ++t) {
+    for (t += ((t - lo) & 1) != set; t < e; t += kSets) {
       const int i = t - lo, st = i % NST;
-      if ((i & 1) != set) continue;
       if (!dead && !mbar_wait(&ctl->full[st], (i / NST) & 1)) {
         report_error(err, MSA_ERR_TIMEOUT, kSiteDenseDecode, blockIdx.x, warp);
         dead = true;
@@ -342,12 +348,12 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int kk = 0; kk < KK; ++kk)
           ldsm_x4(base + (kk >> 2) * line + k_row + ((((kk & 3) * 2 + k_bit) ^ swz) << 4), f[kk]);
         float odd[2][4];
+        mma_16816_first(sc[0], qf[0], f[0][0], f[0][1]);
+        mma_16816_first(sc[1], qf[0], f[0][2], f[0][3]);
+        mma_16816_first(odd[0], qf[1], f[1][0], f[1][1]);
+        mma_16816_first(odd[1], qf[1], f[1][2], f[1][3]);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[n][x] = odd[n][x] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < KK; kk += 2) {
+        for (int kk = 2; kk < KK; kk += 2) {
           mma_16816(sc[0], qf[kk], f[kk][0], f[kk][1]);
           mma_16816(sc[1], qf[kk], f[kk][2], f[kk][3]);
           mma_16816(odd[0], qf[kk + 1], f[kk + 1][0], f[kk + 1][1]);
@@ -381,20 +387,24 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (r + 8 < Hg) dst[32 + lane] = make_float4(sc[0][2], sc[0][3], sc[1][2], sc[1][3]);
       }
       if (valid > 0) {
-        float sub_m[2], fac[2];
+        float top[2], sub_m[2];
         bool grew = false;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           float mx = fmaxf(fmaxf(sc[0][2 * y], sc[0][2 * y + 1]), fmaxf(sc[1][2 * y], sc[1][2 * y + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[y], mx * c);
-          sub_m[y] = mn == -INFINITY ? 0.f : mn;               // no key yet: 2^(-inf - 0) = 0
-          fac[y] = ex2_approx(m[y] - sub_m[y]);
-          grew |= mn > m[y];
-          m[y] = mn;
+          top[y] = mx * c;
+          grew |= top[y] > m[y] + kSlack;
         }
         if (__any_sync(0xffffffffu, grew)) {
+          float fac[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const bool up = top[y] > m[y] + kSlack;
+            fac[y] = up ? ex2_approx(m[y] - top[y]) : 1.f;
+            if (up) m[y] = top[y];
+          }
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -402,6 +412,8 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           l[0] *= fac[0];
           l[1] *= fac[1];
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sub_m[y] = m[y] == -INFINITY ? 0.f : m[y];   // no key yet: 2^(-inf - 0) = 0
         uint32_t ph[4], pl[4];                                  // value and remainder of the weights
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -447,6 +459,7 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       if (lane == 0) mbar_arrive(&ctl->empty[st]);
     }
 
+    t = e;
     // ---- the warps' sums of this part of the sequence become one per group
 #pragma unroll
     for (int y = 0; y < 2; ++y) {

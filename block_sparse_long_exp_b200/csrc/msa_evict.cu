@@ -768,14 +768,12 @@ int launch_long_select(const EvictSelectArgs& s, cudaStream_t st) {
   a.rows = (int32_t)rows; a.err = s.err;
   const dim3 grid((unsigned)(rows * L.parts));
   const int64_t clear = (3 * rows * 512 + kLongThreads - 1) / kLongThreads;
+  ProfScope p("evict_select", st);                // all six
+  prof_count_launch(5);
   long_clear_kernel<<<(unsigned)(clear < 592 ? clear : 592), kLongThreads, 0, st>>>(a);
   int rc = (int)cudaGetLastError();
-  prof_count_launch(5);
-  if (rc == 0) {
-    ProfScope p("evict_select", st);
-    auto* keys = R == s.G ? long_keys_kernel<1> : s.G == 2 ? long_keys_kernel<2> : long_keys_kernel<4>;
-    rc = launch_after(keys, grid, kLongThreads, st, a);
-  }
+  auto* keys = R == s.G ? long_keys_kernel<1> : s.G == 2 ? long_keys_kernel<2> : long_keys_kernel<4>;
+  if (rc == 0) rc = launch_after(keys, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_hist_kernel<1>, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_hist_kernel<2>, grid, kLongThreads, st, a);
   if (rc == 0) rc = launch_after(long_count_kernel, grid, kLongThreads, st, a);
