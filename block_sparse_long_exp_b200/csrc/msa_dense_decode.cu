@@ -338,6 +338,10 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       if (dead) continue;
       const int valid = ctl->valid[st] - sub * kTileTok;      // tokens of this warp to attend
+      auto release = [&] {                                     // the warp's part of the stage is in its registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->empty[st]);
+      };
       float sc[2][4];                                          // scores: tokens 0-7 and 8-15 of the warp
       const uint32_t base = smem0 + st * STAGE + grp;
       uint32_t f[KK][4];                                       // the keys' fragments, then the values'
@@ -429,6 +433,7 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
         for (int n2 = KK / 2; n2 < KK; ++n2)     // (all of them ahead of the softmax would not fit in the registers)
           ldsm_x4_trans(base + KV + (n2 >> 2) * line + v_row + ((((n2 & 3) * 2 + v_bit) ^ swz) << 4), f[n2]);
+        release();
         // value rows past the last token may hold anything (0 x inf is no 0): cleared in the operand
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (valid < kTileTok) {
@@ -454,9 +459,9 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           mma_16816(o[2 * n2], pl, f[n2][0], f[n2][1]);
           mma_16816(o[2 * n2 + 1], pl, f[n2][2], f[n2][3]);
         }
+      } else {
+        release();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->empty[st]);
     }
 
     t = e;
