@@ -1006,20 +1006,15 @@ class _on:
     """The device of a call's tensors made current, and its stream: `with` gives
     the stream's handle.  What is allocated inside belongs to that stream, so
     that a workspace or output released after an unchecked call on a side stream
-    is not handed out while the call still runs.  With the current stream of the
-    current device, as most calls have it, nothing is switched: a switch costs
-    5 us of a call that may take ten."""
+    is not handed out while the call still runs."""
     __slots__ = ("device", "stream", "stack")
 
     def __init__(self, device, stream):
         if stream is not None and stream.device != device:
             raise MsaError(f"stream of {stream.device}, tensors on {device}")
-        self.device, self.stream, self.stack = device, stream, None
+        self.device, self.stream, self.stack = device, stream, contextlib.ExitStack()
 
     def __enter__(self) -> int:
-        if self.stream is None and self.device.index == torch.cuda.current_device():
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
-        self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(self.device))
         if self.stream is None:
             return torch.cuda.current_stream().cuda_stream
@@ -1027,8 +1022,40 @@ class _on:
         return self.stream.cuda_stream
 
     def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
+        self.stack.close()
+
+
+# A call of the cache's functions below may take 6 us on the device, so the host's part is kept short: one pass over the
+# arguments that says whether all is as it must be (where not, _arg and _require_cuda name what), and no switch of device
+# or stream where the call runs on the current ones.
+
+def _is(t, dtype: torch.dtype, shape, dev: int) -> bool:
+    """t is a plain contiguous tensor of this type and shape on CUDA device dev."""
+    return type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+        and t.get_device() == dev >= 0
+
+
+def _are_on(dev: int, ws, keep) -> bool:
+    """The workspace (or None) and a description's tensors are on device dev."""
+    if ws is not None and not (type(ws) is torch.Tensor and ws.is_contiguous() and ws.get_device() == dev):
+        return False
+    for t in keep:
+        if t.get_device() != dev:
+            return False
+    return True
+
+
+def _where(t) -> int:
+    """The CUDA device of a tensor (-1: none)."""
+    return t.get_device() if type(t) is torch.Tensor else -1
+
+
+def _launch(call, dev: int, tensor, stream, *args):
+    """call(*args, handle, stream) with the call's device and stream current."""
+    if stream is None and dev == torch._C._cuda_getDevice():
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev), None)
+    with _on(tensor.device, stream) as handle:
+        return call(*args, handle, stream)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -1061,36 +1088,43 @@ def msa_dense_attn_decode_paged(shape: Shape, pages: Paged, q: torch.Tensor, k_p
     plus each key's attention weight summed over its group's heads, in place
     (entries past a sequence's end stay).  A length of 0 is a padded row: out 0,
     lse -inf."""
-    lib = load_library()
     B, rows, H, G, d = pages.batch, pages.num_pages * 128, shape.H, shape.G, shape.d
-    _arg("q", q, torch.bfloat16, (B, H, d))
-    _arg("k_pages", k_pages, torch.bfloat16, (rows, G, d))
-    _arg("v_pages", v_pages, torch.bfloat16, (rows, G, d))
-    if out is not None:
-        _arg("out", out, torch.bfloat16, (B, H, d))
-    if lse is not None:
-        _arg("lse", lse, torch.float32, (B, H))
-    if weights is not None:
-        _arg("weights", weights, torch.float32, (B, G, pages.max_blocks * 128))
-    decay = _decay(decay)
-    _ws_arg(ws)
-    _require_cuda(q, k_pages, v_pages, out, lse, weights, ws, *getattr(pages, "_keep", ()))
-    with _on(q.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = q.new_empty((B, H), dtype=torch.float32)
-        if ws is None:
-            need = msa_dense_attn_decode_paged_workspace_size(shape, pages, weights is not None)
-            if need == 0:
-                raise MsaError("msa_dense_attn_decode_paged: shape or paged description rejected")
-            ws = _workspace(need, q.device)
-        rc = lib.msa_dense_attn_decode_paged(ctypes.byref(shape), ctypes.byref(pages), _at(q), _at(k_pages),
-                                             _at(v_pages), _at(out), _at(lse), _at(weights), decay, _at(ws),
-                                             _nbytes(ws), handle)
+    decay, dev, keep, kv = _decay(decay), _where(q), getattr(pages, "_keep", ()), (rows, G, d)
+    if not (_is(q, torch.bfloat16, (B, H, d), dev) and _is(k_pages, torch.bfloat16, kv, dev)
+            and _is(v_pages, torch.bfloat16, kv, dev) and (out is None or _is(out, torch.bfloat16, (B, H, d), dev))
+            and (lse is None or _is(lse, torch.float32, (B, H), dev))
+            and (weights is None or _is(weights, torch.float32, (B, G, pages.max_blocks * 128), dev))
+            and _are_on(dev, ws, keep)):
+        _arg("q", q, torch.bfloat16, (B, H, d))
+        _arg("k_pages", k_pages, torch.bfloat16, kv)
+        _arg("v_pages", v_pages, torch.bfloat16, kv)
+        _arg("out", out, torch.bfloat16, (B, H, d), optional=True)
+        _arg("lse", lse, torch.float32, (B, H), optional=True)
+        _arg("weights", weights, torch.float32, (B, G, pages.max_blocks * 128), optional=True)
+        _ws_arg(ws)
+        _require_cuda(q, k_pages, v_pages, out, lse, weights, ws, *keep)
+        dev = q.get_device()
+    return _launch(_dense_decode, dev, q, stream, shape, pages, q, k_pages, v_pages, out, lse, want_lse, weights, decay,
+                   ws, check)
+
+
+def _dense_decode(shape, pages, q, k_pages, v_pages, out, lse, want_lse, weights, decay, ws, check, handle, stream):
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = q.new_empty((q.shape[0], q.shape[1]), dtype=torch.float32)
+    if ws is None:
+        need = msa_dense_attn_decode_paged_workspace_size(shape, pages, weights is not None)
+        if need == 0:
+            raise MsaError("msa_dense_attn_decode_paged: shape or paged description rejected")
+        ws = _workspace(need, q.device)
+    rc = load_library().msa_dense_attn_decode_paged(
+        ctypes.byref(shape), ctypes.byref(pages), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+        _at(lse), _at(weights), decay, ws.data_ptr(), ws.nbytes, handle)
+    if rc != MSA_OK:
         _check(rc, "msa_dense_attn_decode_paged")
-        if check:
-            _device_check(ws, stream, "msa_dense_attn_decode_paged")
+    if check:
+        _device_check(ws, stream, "msa_dense_attn_decode_paged")
     return out, lse
 
 
@@ -1107,31 +1141,48 @@ def msa_attn_weights(shape: Shape, seqs: Varlen, q: torch.Tensor, k: torch.Tenso
     decay * weights + sum over queries and the group's heads of exp(s - lse),
     lse [total_q, H] from msa_dense_attn.  weights=None starts from zeros of
     width max S_b.  Returns weights."""
-    lib = load_library()
-    B, G = seqs.batch, shape.G
-    _arg("q", q, torch.bfloat16, (seqs.total_q, shape.H, shape.d))
-    _arg("k", k, torch.bfloat16, (seqs.total_k, G, shape.d))
-    _arg("lse", lse, torch.float32, (seqs.total_q, shape.H))
-    _arg("weights", weights, torch.float32, optional=True)
-    if weights is not None and (weights.dim() != 3 or tuple(weights.shape[:2]) != (B, G) or
-                                weights.shape[2] < seqs.max_k_len):
-        raise MsaError(f"weights: shape {tuple(weights.shape)}, expected ({B}, {G}, {seqs.max_k_len} or more)")
-    decay = _decay(decay)
-    _ws_arg(ws)
-    _require_cuda(q, k, lse, weights, ws, *getattr(seqs, "_keep", ()))
-    with _on(q.device, stream) as handle:
-        if weights is None:
-            weights = torch.zeros((B, G, seqs.max_k_len), dtype=torch.float32, device=q.device)
-        if ws is None:
-            need = msa_attn_weights_workspace_size(shape, seqs)
-            if need == 0:
-                raise MsaError("msa_attn_weights: shape or sequence description rejected")
-            ws = _workspace(need, q.device)
-        rc = lib.msa_attn_weights(ctypes.byref(shape), ctypes.byref(seqs), _at(q), _at(k), _at(lse), _at(weights),
-                                  int(weights.shape[2]), decay, _at(ws), _nbytes(ws), handle)
+    B, G, H, d = seqs.batch, shape.G, shape.H, shape.d
+    T, S = seqs.total_q, seqs.total_k
+    decay, dev, keep = _decay(decay), _where(q), getattr(seqs, "_keep", ())
+    if not (_is(q, torch.bfloat16, (T, H, d), dev) and _is(k, torch.bfloat16, (S, G, d), dev)
+            and _is(lse, torch.float32, (T, H), dev)
+            and (weights is None or _is(weights, torch.float32, getattr(weights, "shape", None), dev))
+            and _are_on(dev, ws, keep)):
+        _arg("q", q, torch.bfloat16, (T, H, d))
+        _arg("k", k, torch.bfloat16, (S, G, d))
+        _arg("lse", lse, torch.float32, (T, H))
+        _arg("weights", weights, torch.float32, optional=True)
+        _ws_arg(ws)
+        if weights is not None:
+            _rows_of_weights(weights, B, G, seqs.max_k_len)
+        _require_cuda(q, k, lse, weights, ws, *keep)
+        dev = q.get_device()
+    if weights is not None:
+        _rows_of_weights(weights, B, G, seqs.max_k_len)
+    return _launch(_attn_weights, dev, q, stream, shape, seqs, q, k, lse, weights, decay, ws, check)
+
+
+def _rows_of_weights(weights: torch.Tensor, B: int, G: int, most: int):
+    at = weights.shape
+    if len(at) != 3 or at[0] != B or at[1] != G or at[2] < most:
+        raise MsaError(f"weights: shape {tuple(at)}, expected ({B}, {G}, {most} or more)")
+
+
+def _attn_weights(shape, seqs, q, k, lse, weights, decay, ws, check, handle, stream):
+    if weights is None:
+        weights = torch.zeros((seqs.batch, shape.G, seqs.max_k_len), dtype=torch.float32, device=q.device)
+    if ws is None:
+        need = msa_attn_weights_workspace_size(shape, seqs)
+        if need == 0:
+            raise MsaError("msa_attn_weights: shape or sequence description rejected")
+        ws = _workspace(need, q.device)
+    rc = load_library().msa_attn_weights(ctypes.byref(shape), ctypes.byref(seqs), q.data_ptr(), k.data_ptr(),
+                                         lse.data_ptr(), weights.data_ptr(), weights.shape[2], decay, ws.data_ptr(),
+                                         ws.nbytes, handle)
+    if rc != MSA_OK:
         _check(rc, "msa_attn_weights")
-        if check:
-            _device_check(ws, stream, "msa_attn_weights")
+    if check:
+        _device_check(ws, stream, "msa_attn_weights")
     return weights
 
 
@@ -1151,32 +1202,42 @@ def msa_evict_select(shape: Shape, pages: Paged, weights: torch.Tensor, budget: 
     with per_group each group by its own), ties to the lower position.  Returns
     kept int32 [batch, G if per_group else 1, budget] (ascending, -1 padded) and
     new_lens int32 [batch]."""
-    lib = load_library()
-    B, R, budget = pages.batch, shape.G if per_group else 1, int(budget)
+    B, R, budget, n_sink, n_recent = pages.batch, shape.G if per_group else 1, int(budget), int(n_sink), int(n_recent)
     if budget < 1 or n_sink < 0 or n_recent < 0 or n_sink + n_recent > budget or budget >= 2 ** 31:
         raise MsaError(f"msa_evict_select: budget {budget}, n_sink {n_sink}, n_recent {n_recent}: expected "
                        "budget >= 1 and n_sink + n_recent <= budget")
-    _arg("weights", weights, torch.float32, (B, shape.G, pages.max_blocks * 128))
-    _arg("kept", kept, torch.int32, (B, R, budget), optional=True)
-    _arg("new_lens", new_lens, torch.int32, (B,), optional=True)
-    _ws_arg(ws)
-    _require_cuda(weights, kept, new_lens, ws, *getattr(pages, "_keep", ()))
-    with _on(weights.device, stream) as handle:
-        if kept is None:
-            kept = weights.new_empty((B, R, budget), dtype=torch.int32)
-        if new_lens is None:
-            new_lens = weights.new_empty((B,), dtype=torch.int32)
-        if ws is None:
-            need = msa_evict_select_workspace_size(shape, pages, per_group)
-            if need == 0:
-                raise MsaError("msa_evict_select: shape or paged description rejected")
-            ws = _workspace(need, weights.device)
-        rc = lib.msa_evict_select(ctypes.byref(shape), ctypes.byref(pages), _at(weights), budget, int(n_sink),
-                                  int(n_recent), 1 if per_group else 0, _at(kept), _at(new_lens), _at(ws),
-                                  _nbytes(ws), handle)
+    dev, keep = _where(weights), getattr(pages, "_keep", ())
+    at = (B, shape.G, pages.max_blocks * 128)
+    if not (_is(weights, torch.float32, at, dev) and (kept is None or _is(kept, torch.int32, (B, R, budget), dev))
+            and (new_lens is None or _is(new_lens, torch.int32, (B,), dev)) and _are_on(dev, ws, keep)):
+        _arg("weights", weights, torch.float32, at)
+        _arg("kept", kept, torch.int32, (B, R, budget), optional=True)
+        _arg("new_lens", new_lens, torch.int32, (B,), optional=True)
+        _ws_arg(ws)
+        _require_cuda(weights, kept, new_lens, ws, *keep)
+        dev = weights.get_device()
+    return _launch(_evict_select, dev, weights, stream, shape, pages, weights, budget, n_sink, n_recent, R, per_group, kept,
+                   new_lens, ws, check)
+
+
+def _evict_select(shape, pages, weights, budget, n_sink, n_recent, R, per_group, kept, new_lens, ws, check, handle, stream):
+    B = pages.batch
+    if kept is None:
+        kept = weights.new_empty((B, R, budget), dtype=torch.int32)
+    if new_lens is None:
+        new_lens = weights.new_empty((B,), dtype=torch.int32)
+    if ws is None:
+        need = msa_evict_select_workspace_size(shape, pages, per_group)
+        if need == 0:
+            raise MsaError("msa_evict_select: shape or paged description rejected")
+        ws = _workspace(need, weights.device)
+    rc = load_library().msa_evict_select(ctypes.byref(shape), ctypes.byref(pages), weights.data_ptr(), budget, n_sink,
+                                         n_recent, 1 if per_group else 0, kept.data_ptr(), new_lens.data_ptr(),
+                                         ws.data_ptr(), ws.nbytes, handle)
+    if rc != MSA_OK:
         _check(rc, "msa_evict_select")
-        if check:
-            _device_check(ws, stream, "msa_evict_select")
+    if check:
+        _device_check(ws, stream, "msa_evict_select")
     return kept, new_lens
 
 
@@ -1197,39 +1258,58 @@ def msa_evict_move(shape: Shape, pages: Paged, new_pages: Paged, kept: torch.Ten
     kept tokens' weights, zeros from the new length on.  Returns weights_out.
     The old pages keep their rows; a new page that is also an old one, or named
     twice, is reported and not written."""
-    lib = load_library()
-    B, rows, G = pages.batch, pages.num_pages * 128, shape.G
+    B, rows, G, d = pages.batch, pages.num_pages * 128, shape.G, shape.d
     if new_pages.batch != B or new_pages.num_pages != pages.num_pages:
         raise MsaError("msa_evict_move: pages and new_pages describe the same sequences and pool "
                        f"(batch {B} and {new_pages.batch}, num_pages {pages.num_pages} and {new_pages.num_pages})")
-    _arg("kept", kept, torch.int32)
-    if kept.dim() != 3 or kept.shape[0] != B or kept.shape[1] not in (1, G) or kept.shape[2] < 1:
-        raise MsaError(f"kept: shape {tuple(kept.shape)}, expected ({B}, 1 or {G}, width)")
-    per_group = kept.shape[1] == G and G > 1
-    if per_group and k_idx_pages is not None:
+    dev, keep = _where(kept), (*getattr(pages, "_keep", ()), *getattr(new_pages, "_keep", ()))
+    w_at, out_at = (B, G, pages.max_blocks * 128), (B, G, new_pages.max_blocks * 128)
+    kv, ki = (rows, G, d), (rows, shape.d_idx)
+    if not (_is(kept, torch.int32, kept.shape if dev >= 0 else None, dev) and _is(k_pages, torch.bfloat16, kv, dev)
+            and _is(v_pages, torch.bfloat16, kv, dev)
+            and (k_idx_pages is None or _is(k_idx_pages, torch.bfloat16, ki, dev))
+            and (weights is None or _is(weights, torch.float32, w_at, dev))
+            and (weights_out is None or _is(weights_out, torch.float32, out_at, dev)) and _are_on(dev, ws, keep)):
+        _arg("kept", kept, torch.int32)
+        _rows_of_kept(kept, B, G, k_idx_pages, weights, weights_out)
+        _arg("k_pages", k_pages, torch.bfloat16, kv)
+        _arg("v_pages", v_pages, torch.bfloat16, kv)
+        _arg("k_idx_pages", k_idx_pages, torch.bfloat16, ki, optional=True)
+        _arg("weights", weights, torch.float32, w_at, optional=True)
+        _arg("weights_out", weights_out, torch.float32, out_at, optional=True)
+        _ws_arg(ws)
+        _require_cuda(kept, k_pages, v_pages, k_idx_pages, weights, weights_out, ws, *keep)
+        dev = kept.get_device()
+    _rows_of_kept(kept, B, G, k_idx_pages, weights, weights_out)
+    return _launch(_evict_move, dev, kept, stream, shape, pages, new_pages, kept, k_pages, v_pages, k_idx_pages, weights,
+                   weights_out, out_at, ws, check)
+
+
+def _rows_of_kept(kept, B: int, G: int, k_idx_pages, weights, weights_out):
+    at = kept.shape
+    if len(at) != 3 or at[0] != B or at[1] not in (1, G) or at[2] < 1:
+        raise MsaError(f"kept: shape {tuple(at)}, expected ({B}, 1 or {G}, width)")
+    if at[1] > 1 and k_idx_pages is not None:
         raise MsaError("msa_evict_move: the groups share the index keys; a ranking per group has none to move")
     if weights is None and weights_out is not None:
         raise MsaError("msa_evict_move: weights_out without weights")
-    _arg("k_pages", k_pages, torch.bfloat16, (rows, G, shape.d))
-    _arg("v_pages", v_pages, torch.bfloat16, (rows, G, shape.d))
-    _arg("k_idx_pages", k_idx_pages, torch.bfloat16, (rows, shape.d_idx), optional=True)
-    _arg("weights", weights, torch.float32, (B, G, pages.max_blocks * 128), optional=True)
-    _arg("weights_out", weights_out, torch.float32, (B, G, new_pages.max_blocks * 128), optional=True)
-    _ws_arg(ws)
-    _require_cuda(kept, k_pages, v_pages, k_idx_pages, weights, weights_out, ws, *getattr(pages, "_keep", ()),
-                  *getattr(new_pages, "_keep", ()))
-    with _on(kept.device, stream) as handle:
-        if weights is not None and weights_out is None:
-            weights_out = torch.empty((B, G, new_pages.max_blocks * 128), dtype=torch.float32, device=kept.device)
-        if ws is None:
-            need = msa_evict_move_workspace_size(shape, pages)
-            if need == 0:
-                raise MsaError("msa_evict_move: shape or paged description rejected")
-            ws = _workspace(need, kept.device)
-        rc = lib.msa_evict_move(ctypes.byref(shape), ctypes.byref(pages), ctypes.byref(new_pages), _at(kept),
-                                int(kept.shape[2]), 1 if per_group else 0, _at(k_pages), _at(v_pages),
-                                _at(k_idx_pages), _at(weights), _at(weights_out), _at(ws), _nbytes(ws), handle)
+
+
+def _evict_move(shape, pages, new_pages, kept, k_pages, v_pages, k_idx_pages, weights, weights_out, out_at, ws, check,
+                handle, stream):
+    if weights is not None and weights_out is None:
+        weights_out = torch.empty(out_at, dtype=torch.float32, device=kept.device)
+    if ws is None:
+        need = msa_evict_move_workspace_size(shape, pages)
+        if need == 0:
+            raise MsaError("msa_evict_move: shape or paged description rejected")
+        ws = _workspace(need, kept.device)
+    rc = load_library().msa_evict_move(
+        ctypes.byref(shape), ctypes.byref(pages), ctypes.byref(new_pages), kept.data_ptr(), kept.shape[2],
+        1 if kept.shape[1] > 1 else 0, k_pages.data_ptr(), v_pages.data_ptr(), _at(k_idx_pages), _at(weights),
+        _at(weights_out), ws.data_ptr(), ws.nbytes, handle)
+    if rc != MSA_OK:
         _check(rc, "msa_evict_move")
-        if check:
-            _device_check(ws, stream, "msa_evict_move")
+    if check:
+        _device_check(ws, stream, "msa_evict_move")
     return weights_out

@@ -151,7 +151,8 @@ def test_binding_checks_the_key_weights(M):
     for match, call in (
             ("q: shape", lambda: f(shape, seqs, _bf(9, H, d), k, lse)), ("k: dtype", lambda: f(shape, seqs, q, k.float(), lse)),
             ("lse: shape", lambda: f(shape, seqs, q, k, torch.zeros(H, 10))),
-            ("lse: a tensor", lambda: f(shape, seqs, q, k, None)),
+            ("lse: a tensor", lambda: f(shape, seqs, q, k, None)), ("weights: expected a torch", lambda: f(shape, seqs, q, k, lse, weights=5)),
+            ("q: expected a torch", lambda: f(shape, seqs, [1.0], k, lse)),
             ("weights: shape", lambda: f(shape, seqs, q, k, lse, weights=torch.zeros(1, G, 29))),
             ("weights: shape", lambda: f(shape, seqs, q, k, lse, weights=torch.zeros(1, H, 30))),
             ("weights: dtype", lambda: f(shape, seqs, q, k, lse, weights=torch.zeros(1, G, 30).double())),
@@ -177,7 +178,8 @@ def test_binding_checks_the_eviction(M):
             ("CUDA", lambda: s(shape, pg, w, 100)),
             ("same sequences", lambda: m(shape, pg, _pages(M, batch=3), kept, kv, kv)),
             ("same sequences", lambda: m(shape, pg, _pages(M, num_pages=21), kept, kv, kv)),
-            ("kept: dtype", lambda: m(shape, pg, new, kept.long(), kv, kv)),
+            ("kept: dtype", lambda: m(shape, pg, new, kept.long(), kv, kv)), ("kept: a tensor", lambda: m(shape, pg, new, None, kv, kv)),
+            ("weights: expected a torch", lambda: s(shape, pg, 3.0, 10)),
             ("kept: shape", lambda: m(shape, pg, new, kept[0], kv, kv)),
             ("kept: shape", lambda: m(shape, pg, new, torch.zeros(2, 3, 100, dtype=torch.int32), kv, kv)),
             ("index keys", lambda: m(shape, pg, new, kept_g, kv, kv, k_idx_pages=ki)),
