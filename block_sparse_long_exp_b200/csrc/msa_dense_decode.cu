@@ -11,8 +11,8 @@
 //
 // The step is bound by HBM: every cached key and value is read once and meets
 // H / G query heads, 16 operations a byte at most.  On a B200 (H 64, G 4, d 128):
-// 32 caches of 1..8192 tokens 57.8 us (283 MB; 43 at the rate of a copy), one of
-// 1M 335 us on a cool device (6.4 TB/s) and 378 in a row, at the board's power
+// 32 caches of 1..8192 tokens 55.7 us (283 MB; 43 at the rate of a copy), one of
+// 1M 331 us on a cool device (6.5 TB/s) and 372 in a row, at the board's power
 // limit; the loads alone take 306.
 //   split : the caches are cut into tiles of 64 / G tokens with all G groups
 //           (16 KB of keys and as much of values at d = 128, contiguous in the
@@ -32,7 +32,7 @@
 //   weights: the scores are kept in 32 bits (a 16-bit score would be off by
 //           2^-9 of its size, so its weight by per cents) and read again once m
 //           and l are known: 8 H bytes a token next to the 4 G d of K and V.
-//           Reading K again would cost 2 G d.  2 x 262K..400K tokens: 309 us,
+//           Reading K again would cost 2 G d.  2 x 262K..400K tokens: 305 us,
 //           16 x 1K..16K (H 32, G 2) 53.6.
 #include <cuda_runtime.h>
 

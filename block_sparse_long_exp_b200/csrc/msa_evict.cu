@@ -13,7 +13,7 @@
 //   the latency of some fifteen barriers; beyond, a CTA has 4096 tokens and the
 //   steps are launches.  Bound by those launches up to some 300,000 tokens in
 //   all, then by the weights from HBM.  On a B200: 8 x 5K tokens 8.9 us in a
-//   graph (14.1 called one by one), 2 x 1M 33.6 us.
+//   graph (13.5 called one by one), 2 x 1M 34 us.
 // move: the rows of the kept tokens gathered into other pages; reads and writes
 //   each kept byte once (HBM).  Out of place: a page of the source may be shared
 //   with another sequence, and the rows can go in any order.  On a B200: 4 x 64K
