@@ -436,3 +436,31 @@ def test_choice_in_a_graph(M, L):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(kept[:, 0].cpu(), _want_fast(w, lens, 900, 3, 40)) and new.cpu().tolist() == [min(n, 900) for n in lens]
+
+
+@pytest.mark.parametrize("L", [3000, 30000, 90000])
+def test_two_calls_at_once(M, L):
+    # choice and move on two streams, each with a workspace and pages of its own
+    blocks, budget = -(-L // PAGE), 500
+    shape = M.make_shape(8, 2, 64, 32, 16)
+    pages = blocks + 4
+    pool = _pool(2, 64, 32, pages, 41)
+    table, new_table = torch.arange(blocks, dtype=torch.int32)[None], blocks + torch.arange(4, dtype=torch.int32)[None]
+    ws = [_weights(1, 2, blocks, 42 + i) for i in range(2)]
+    wd, dev = [w.cuda() for w in ws], [[x.cuda() for x in pool] for _ in range(2)]
+    pg = [M.make_paged(torch.tensor([L], dtype=torch.int32).cuda(), table.cuda(), L, pages) for _ in range(2)]
+    nt = new_table.cuda()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            kept, new = M.msa_evict_select(shape, pg[i], wd[i], budget, 3, 40, stream=st, check=False)
+            out = M.msa_evict_move(shape, pg[i], M.make_paged(new, nt, budget, pages), kept, dev[i][0], dev[i][1],
+                                   k_idx_pages=dev[i][2], weights=wd[i], stream=st, check=False)
+            got[i] = (kept, out)
+    torch.cuda.synchronize()
+    for i in range(2):
+        kept, out = got[i]
+        assert torch.equal(kept[:, 0].cpu(), _want_fast(ws[i], [L], budget, 3, 40))
+        k, v, ki, want = _moved(pool, table, new_table, kept.cpu(), [budget], ws[i], 512)
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(dev[i], (k, v, ki))) and torch.equal(out.cpu(), want)
