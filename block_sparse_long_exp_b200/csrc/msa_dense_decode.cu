@@ -150,14 +150,71 @@ struct SeqLens {
   }
 };
 
+// What a CTA has summed of a sequence, where something came out infinite or NaN (a
+// cache with such a value, or one too large: seldom).  The two terms of a softmax
+// weight meet a value v separately, and that breaks an infinite one: a remainder of
+// 0 times inf is NaN, a negative one gives inf - inf.  So the warp that has a group's
+// sums reads the values of the tiles [first, end) again from their pages, and a column
+// that has one that is not finite gets what the formula says for weights above 0:
+// that infinity, or NaN for both signs or a NaN: written over what the warp has
+// stored, row y of the lane (r, r + 8) where bit y of `rows` says so, to `out` or, of a
+// part, to `part`.  Lane (r, c2 / 2) reads the tokens r, r + 8, ... of a tile in its
+// own columns.  (Not inlined, and in memory: 32 x 1..8192 tokens, H 64, G 4, d 128, take
+// 53.1 us so and 57.6 with it among the main loop's registers.)
+template <int D>
+__device__ __noinline__ void put_infinities(const __nv_bfloat16* __restrict__ v_pages, int G, int g,
+                                            const int32_t* __restrict__ table, int64_t num_pages, int L, int first, int end,
+                                            __nv_bfloat16* out, float* part, uint32_t rows) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c2 = 2 * (lane & 3);
+  const int tok = 64 / G;
+  uint32_t pos = 0, neg = 0;                     // a bit per column of the lane: 2 n + parity
+  for (int t = first; t < end; ++t) {            // tiles of the sequence
+    const int j0 = t * tok, page = table[j0 / kBk];
+    if (page < 0 || page >= num_pages) continue;
+    for (int x = r; x < min(tok, L - j0); x += 8) {
+      const int64_t row = (int64_t)page * kBk + (j0 & (kBk - 1)) + x;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(v_pages + (row * G + g) * D + c2);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const uint32_t two = src[4 * n];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t u = y == 0 ? two & 0xffffu : two >> 16, bit = 1u << (2 * n + y);
+          if ((u & 0x7f80u) != 0x7f80u) continue;
+          const bool nan = (u & 0x7fu) != 0;
+          if (nan || u < 0x8000u) pos |= bit;
+          if (nan || u >= 0x8000u) neg |= bit;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 4; x <= 16; x <<= 1) {
+    pos |= __shfl_xor_sync(0xffffffffu, pos, x);
+    neg |= __shfl_xor_sync(0xffffffffu, neg, x);
+  }
+  for (int y = 0; y < 2; ++y) {
+    if ((rows >> y & 1u) == 0) continue;
+    for (int i = 0; i < D / 4; ++i) {
+      const uint32_t bit = 1u << i;
+      if (((pos | neg) & bit) == 0) continue;
+      const float v = pos & neg & bit ? __uint_as_float(0x7fffffffu) : pos & bit ? INFINITY : -INFINITY;
+      const int at = (r + 8 * y) * D + 8 * (i >> 1) + c2 + (i & 1);
+      if (out != nullptr) out[at] = __float2bfloat16_rn(v);
+      else part[at] = v;
+    }
+  }
+}
+
 // kFew: at most eight heads a group.  The rows that they leave of the second
 // product's operand then hold the remainders: one product does for both terms (8 x
 // 64K tokens, H 32, G 4, d 128: 171 us; 178 with two).
 template <int D, bool kWeights, bool kFew>
 __global__ void __launch_bounds__(kDecThreads, 1)
 dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-                    int batch, int H, int G, float sm_scale, const int32_t* __restrict__ seqlens,
+                    const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ v_pages,
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int batch, int H, int G, float sm_scale,
+                    const int32_t* __restrict__ seqlens,
                     const int32_t* __restrict__ block_table, int max_blocks, int max_seqlen, int64_t num_pages,
                     float2* __restrict__ stats, float2* __restrict__ part_ml, float* __restrict__ part_o,
                     float* __restrict__ logits, int logit_tiles, DevError* errors) {
@@ -532,6 +589,12 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
     }
     if (part == 0) {
+      float size[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int x = 0; x < 2 * NY; ++x) size[x] += fabsf(o[n][x]);
+      const bool odd = __any_sync(0xffffffffu, !((size[0] + size[1]) + (size[2] + size[3]) <= 3.402823466e38f));
       const bool whole = t0 == s && e == s + nt;
       const int slot = t0 == s ? 1 : 0;
 #pragma unroll
@@ -540,15 +603,17 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (hl >= Hg) continue;
         const int h = g * Hg + hl;
         if (whole) {
-          // no weight at all (every score -inf): zeros
-          const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
+          // no weight at all (every score -inf): zeros, whatever the values are
+          const bool none = l[y] == 0.f;
+          const float inv = none ? 0.f : 1.f / l[y];
           __nv_bfloat16* dst = out + ((int64_t)b * H + h) * D + c2;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<uint32_t*>(dst + 8 * n) = pack_bf16x2(o[n][2 * y] * inv, o[n][2 * y + 1] * inv);
+            *reinterpret_cast<uint32_t*>(dst + 8 * n) =
+                none ? 0u : pack_bf16x2(o[n][2 * y] * inv, o[n][2 * y + 1] * inv);
           if ((lane & 3) == 0) {
             if (lse != nullptr)
-              lse[(int64_t)b * H + h] = l[y] == 0.f ? -INFINITY : (m[y] + log2f(l[y])) * kLn2;
+              lse[(int64_t)b * H + h] = none ? -INFINITY : (m[y] + log2f(l[y])) * kLn2;
             if constexpr (kWeights) stats[(int64_t)b * H + h] = make_float2(m[y], l[y]);
           }
         } else {
@@ -559,6 +624,12 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * y], o[n][2 * y + 1]);
           if ((lane & 3) == 0) part_ml[at] = make_float2(m[y], l[y]);
         }
+      }
+      if (odd) {                                  // (a row without any weight keeps its zeros)
+        const uint32_t rows = (r < Hg && !(whole && l[0] == 0.f) ? 1u : 0u) | (r + 8 < Hg && !(whole && l[1] == 0.f) ? 2u : 0u);
+        put_infinities<D>(v_pages, G, g, block_table + (int64_t)b * max_blocks, num_pages, L, t0 - s, e - s,
+                          whole ? out + ((int64_t)b * H + g * Hg) * D : nullptr,
+                          part_o + (((int64_t)blockIdx.x * 2 + slot) * H + g * Hg) * D, rows);
       }
     }
   }
@@ -728,9 +799,9 @@ dense_join_kernel(__nv_bfloat16* __restrict__ out, float* __restrict__ lse, int 
       for (int u = 0; u < WPJ; ++u) o[x] += acc[u][VEC * lane + x];
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = 1.f / l;
 #pragma unroll
-  for (int x = 0; x < VEC; ++x) o[x] *= inv;
+  for (int x = 0; x < VEC; ++x) o[x] = l == 0.f ? 0.f : o[x] * inv;   // no weight at all: zeros, whatever the values are
   store(o);
   if (lane == 0 && blockIdx.x % CB == 0) {
     if (lse != nullptr) lse[pair] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -809,9 +880,9 @@ int launch_split(const DenseDecodeArgs& a, int ctas, const CUtensorMap& tm_k, co
   if (rc != 0) return rc;
   ProfScope p("dense_decode", st);
   dense_decode_kernel<D, kWeights, kFew><<<ctas, kDecThreads, smem, st>>>(
-      tm_k, tm_v, static_cast<const __nv_bfloat16*>(a.q), static_cast<__nv_bfloat16*>(a.out), a.lse, a.batch, a.H, a.G,
-      a.sm_scale, a.seqlens, a.block_table, a.max_blocks, a.max_seqlen, a.num_pages, a.stats, a.part_ml, a.part_o,
-      a.logits, logit_tiles, a.errors);
+      tm_k, tm_v, static_cast<const __nv_bfloat16*>(a.q), static_cast<const __nv_bfloat16*>(a.v_pages),
+      static_cast<__nv_bfloat16*>(a.out), a.lse, a.batch, a.H, a.G, a.sm_scale, a.seqlens, a.block_table, a.max_blocks,
+      a.max_seqlen, a.num_pages, a.stats, a.part_ml, a.part_o, a.logits, logit_tiles, a.errors);
   return (int)cudaGetLastError();
 }
 

@@ -468,7 +468,10 @@ msa_status_t msa_dense_attn(const msa_shape_t* shape, const msa_varlen_t* seqs,
  * recorded as MSA_ERR_DEVICE_CHECK and treated as 0; a page outside the cache
  * too, and its tokens are left out (nothing is read out of range).  Rows of a
  * page past the sequence's end may hold anything.  A head whose scores are all
- * -inf gets out 0 and lse -inf.
+ * -inf gets out 0 and lse -inf, whatever the values are.  An infinity or NaN
+ * among a sequence's values comes through as the formula has it (in its column of
+ * its group alone; as NaN where its weight is below 2^-118 of the largest).  Finite
+ * values may be up to 2^88 in size: the sums of larger ones may overflow.
  * q, k_pages, v_pages and out 16-byte aligned, sm_scale positive and finite, else
  * MSA_ERR_INVALID_ARG.  The parts of a sequence are joined in a fixed order: results are the same from
  * run to run (on one device model).  Workspace: with_weights != 0 adds 4 H
