@@ -31,6 +31,7 @@ GPU_FILE_ORDER = (
     "test_gpu_autograd.py", "test_gpu_group_shard.py", "test_gpu_timeout.py", "test_gpu_block_sizes.py",
     "test_gpu_key_split.py", "test_gpu_prefill_fused.py", "test_gpu_short_items.py",
     "test_gpu_dense_decode.py", "test_gpu_evict.py", "test_gpu_attn_weights.py",
+    "test_gpu_cache_extremes.py",
     "test_zz_no_alloc.py",          # the allocation-free entry point: always the last file
 )
 
