@@ -504,7 +504,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         unpair(s0, s[0], s[1]);
         unpair(s1, s[2], s[3]);
         const float y = ((s[0] + s[1]) + (s[2] + s[3])) - comp, z = acc + y;
-        comp = (z - acc) - y;
+        comp = fabsf(z) <= 3.402823466e38f ? (z - acc) - y : 0.f;     // (past the largest number: inf, and no inf - inf)
         acc = z;
       }
       if (!ok) break;

@@ -1,5 +1,5 @@
 """A densely attended layer's cache at the ends of what its calls allow:
-values that are infinite, NaN or huge, against the fp64 oracle
+values that are infinite, NaN or huge, key weights past the largest number, against the fp64 oracle
 (oracle/dense_cache.py)."""
 import numpy as np
 import pytest
@@ -98,3 +98,35 @@ def test_values_up_to_the_largest_allowed(M, H, G, d):
     shape = M.make_shape(H, G, d, 64, 16)
     out, lse, _ = _decode(M, shape, lens, table, pages, q, k, v)
     _check(out, lse, None, q, seqs, shape.sm_scale)
+
+
+# ------------------------------------------------------------------ key weights
+
+def _cu(lens):
+    return [sum(lens[:i]) for i in range(len(lens) + 1)]
+
+
+def _varlen(M, T, S):
+    return M.make_varlen(torch.tensor(_cu(T), dtype=torch.int32).cuda(), torch.tensor(_cu(S), dtype=torch.int32).cuda(),
+                         _cu(T), _cu(S))
+
+
+@pytest.mark.parametrize("H,G,d", SHAPES)
+@pytest.mark.parametrize("T", [40, 700, 3000])
+def test_weights_past_the_largest_number_are_infinite(M, H, G, d, T):
+    # scores of 0 and log-sum-exps of their own: query 5 gives 2^130, queries 20 .. 30 give 2^126 each, which
+    # only together pass the largest number, the others 1; the keys up to the last of those queries get infinity
+    shape = M.make_shape(H, G, d, 64, 16)
+    q, k = torch.zeros(T, H, d).bfloat16(), torch.zeros(T, G, d).bfloat16()
+    for heavy, last in (({5: 130.0}, 5), ({t: 126.0 for t in range(20, 31)}, 30), ({5: 130.0, T - 1: 130.0}, T - 1)):
+        x = torch.zeros(T)
+        for t, e in heavy.items():
+            x[t] = e
+        lse = (-x * np.log(2.0))[:, None].expand(T, H).contiguous()
+        w = M.msa_attn_weights(shape, _varlen(M, [T], [T]), q.cuda(), k.cuda(), lse.cuda(), decay=0.0).cpu()[0]
+        want = (H // G) * torch.flip(torch.cumsum(torch.flip(torch.exp(-lse[:, 0].double()), [0]), 0), [0])
+        inf = want > 2.0 ** 128 * 1.01
+        assert bool((w[:, inf] == float("inf")).all()) and int(inf.sum()) >= 6
+        # beyond `last` sums of ones: exact but for the exponential's 2^-22 (an argument of 0 has no error)
+        rest = torch.arange(T) > last
+        assert bool(((w[:, rest].double() - want[rest]).abs() <= want[rest] * 2.0 ** -21).all())
