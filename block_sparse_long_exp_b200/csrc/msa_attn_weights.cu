@@ -156,6 +156,22 @@ struct SeqUnits {
   }
 };
 
+// The sequences' offsets on the device, and what bounds them: the rows that the
+// host names and the rows of the weights.  A sequence that reaches past them is
+// reported and has no units: nothing of it is read or written.
+struct Seqs {
+  const int32_t *cu_q, *cu_k;
+  int32_t total_q, total_k, width;                // (a width beyond 32 bits bounds nothing: a length has 31)
+  __device__ bool ok(int b) const {
+    const int64_t q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
+    if (q1 == q0) return k1 >= k0;                // no queries: left as it is
+    return q0 >= 0 && q1 > q0 && q1 <= total_q && k0 >= 0 && k1 <= total_k && q1 - q0 <= k1 - k0 && k1 - k0 <= width;
+  }
+  __device__ SeqUnits units(int b, int qt_log) const {
+    return ok(b) ? SeqUnits(cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b], qt_log) : SeqUnits();
+  }
+};
+
 __device__ __forceinline__ int64_t run_lo(int i, int64_t total, int n) {
   const int64_t q = total / n;
   const int r = (int)(total - q * n);
@@ -169,18 +185,18 @@ __device__ __forceinline__ int run_of(int64_t t, int64_t total, int n) {
 
 // A walk over a run's units.
 struct Walk {
-  const int32_t *cu_q, *cu_k;
+  Seqs seqs;
   int qt_log, G, b, g, kb, ct;
   int q0, k0;                                     // first query and key row of the sequence
   int64_t seq_first, kb_first;                    // unit index of the sequence's and the key block's first unit
   SeqUnits u;
   __device__ void load() {
-    q0 = cu_q[b];
-    k0 = cu_k[b];
-    u = SeqUnits(cu_q[b + 1] - q0, cu_k[b + 1] - k0, qt_log);
+    q0 = seqs.cu_q[b];
+    k0 = seqs.cu_k[b];
+    u = seqs.units(b, qt_log);
   }
-  __device__ void start(const int32_t* cq, const int32_t* ck, int qtl, int groups, int seq, int64_t first, int64_t lo) {
-    cu_q = cq; cu_k = ck; qt_log = qtl; G = groups; b = seq; seq_first = first;
+  __device__ void start(const Seqs& of, int qtl, int groups, int seq, int64_t first, int64_t lo) {
+    seqs = of; qt_log = qtl; G = groups; b = seq; seq_first = first;
     load();
     int64_t off = lo - first;
     g = (int)(off / u.per_group);
@@ -226,8 +242,7 @@ template <int D>
 __global__ void __launch_bounds__(kAwThreads, 1)
 attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                     const float* __restrict__ lse, float* __restrict__ weights, int64_t width, float decay, int batch,
-                    int H, int G, int qt_log, float scale_log2, const int32_t* __restrict__ cu_q,
-                    const int32_t* __restrict__ cu_k, AwOpen* __restrict__ open, float* __restrict__ part,
+                    int H, int G, int qt_log, float scale_log2, const Seqs seqs, AwOpen* __restrict__ open, float* __restrict__ part,
                     DevError* errors) {
   constexpr int NQ = num_q<D>();
   constexpr int KST = k_stage<D>(), QST = q_stage<D>();
@@ -258,9 +273,8 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     int64_t sum = 0;
     int bad = -1;
     for (int b = b0; b < b1; ++b) {
-      const int T = cu_q[b + 1] - cu_q[b], S = cu_k[b + 1] - cu_k[b];
-      if (T < 0 || T > S) bad = b;
-      sum += G * SeqUnits(T, S, qt_log).per_group;
+      if (!seqs.ok(b)) bad = b;
+      sum += G * seqs.units(b, qt_log).per_group;
     }
     int64_t incl = sum;
 #pragma unroll
@@ -285,7 +299,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       fence_mbar_init();
     }
     __syncthreads();
-    if (blockIdx.x == 0 && bad >= 0) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, bad, cu_q[bad + 1] - cu_q[bad]);
+    if (blockIdx.x == 0 && bad >= 0) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, bad, seqs.cu_q[bad + 1] - seqs.cu_q[bad]);
     int64_t before = 0, total = 0;
     for (int w = 0; w < kAwThreads / 32; ++w) {
       if (w < warp) before += ctl->warp_sum[w];
@@ -297,7 +311,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       int64_t s = before;
       int b = b0;
       for (;; ++b) {
-        const int64_t n = G * SeqUnits(cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b], qt_log).per_group;
+        const int64_t n = G * seqs.units(b, qt_log).per_group;
         if (lo < s + n) break;
         s += n;
       }
@@ -323,7 +337,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // -------------------------------------------------------------- loads
     if (lane == 0) {
       Walk w;
-      w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
+      w.start(seqs, qt_log, G, ctl->first_seq, ctl->first_start, lo);
       bool ok = true;
       int nk = 0, nq = 0;                         // key blocks and column tiles loaded
       for (int64_t t = lo; t < hi && ok;) {
@@ -362,7 +376,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const uint64_t kd0 = make_sdesc(smem_u32(k_s), 16, 1024, kSw128);
       const uint64_t qd0 = make_sdesc(smem_u32(q_s), 16, 1024, kSw128);
       Walk w;
-      w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
+      w.start(seqs, qt_log, G, ctl->first_seq, ctl->first_start, lo);
       bool ok = true;
       int nk = 0, n = 0;
       for (int64_t t = lo; t < hi && ok;) {
@@ -401,7 +415,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   } else if (warp == 2) {
     // ----------------------- the columns' log-sum-exps, in units of log2
     Walk w;
-    w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
+    w.start(seqs, qt_log, G, ctl->first_seq, ctl->first_start, lo);
     const int tq = (4 * lane) >> hg_log, h = (4 * lane) & (Hg - 1);   // a lane's four columns share a query
     auto fetch = [&](float4& v) {
       const int q = (w.ct << qt_log) + tq;
@@ -441,7 +455,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const uint32_t col0 = tmem + half * 128 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint64_t scale2 = pair(scale_log2, scale_log2);
     Walk w;
-    w.start(cu_q, cu_k, qt_log, G, ctl->first_seq, ctl->first_start, lo);
+    w.start(seqs, qt_log, G, ctl->first_seq, ctl->first_start, lo);
     int n = 0;
     bool ok = true;
     for (int64_t t = lo; t < hi && ok;) {
@@ -584,9 +598,10 @@ int launch_units(const AttnWeightsArgs& a, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int rc = allow_smem(attn_weights_kernel<D>, smem, &ready);
   if (rc != 0) return rc;
+  const Seqs seqs{a.cu_q, a.cu_k, (int32_t)a.total_q, (int32_t)a.total_k, (int32_t)(a.width < INT32_MAX ? a.width : INT32_MAX)};
   ProfScope p("attn_weights", st);
   attn_weights_kernel<D><<<ctas, kAwThreads, smem, st>>>(
-      tm_k, tm_q, a.lse, a.weights, a.width, a.decay, a.batch, a.H, a.G, qt_log, a.sm_scale * kLog2e, a.cu_q, a.cu_k,
+      tm_k, tm_q, a.lse, a.weights, a.width, a.decay, a.batch, a.H, a.G, qt_log, a.sm_scale * kLog2e, seqs,
       static_cast<AwOpen*>(a.open), a.part, a.errors);
   return (int)cudaGetLastError();
 }

@@ -500,9 +500,12 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
  * are not touched, nor is a sequence without queries.  A (query, head) whose lse
  * is -inf has seen no key and adds nothing.  width >= max_k_len (a paged cache's
  * max_blocks * 128, so that decode steps go on from it), q, k and lse 16-byte
- * aligned, sm_scale positive and finite, else MSA_ERR_INVALID_ARG.  A sequence with more queries than keys is
- * recorded as MSA_ERR_DEVICE_CHECK and left as it is.  Sums are 32-bit and in a
- * fixed order: the same from run to run (on one device model). */
+ * aligned, sm_scale positive and finite, else MSA_ERR_INVALID_ARG.  On the device
+ * a sequence goes by its own two entries of cu_q and cu_k (the first need not be 0):
+ * one with more queries than keys, or that reaches past total_q, total_k or the
+ * weights' width, is recorded as MSA_ERR_DEVICE_CHECK and left as it is (nothing is
+ * read or written out of range).  Sums are 32-bit and in a fixed order: the same
+ * from run to run (on one device model). */
 size_t msa_attn_weights_workspace_size(const msa_shape_t* shape, const msa_varlen_t* seqs);
 
 msa_status_t msa_attn_weights(const msa_shape_t* shape, const msa_varlen_t* seqs,
@@ -734,7 +737,8 @@ msa_status_t msa_profile_read(const char* kernel, double* total_ms, int64_t* cou
  *   221      bounded-wait self-test              231  decode candidate merge
  *   241      dense paged decode (a length, info0 = sequence, info1 = length; a
  *            page, info0 = sequence, info1 = block; a wait)
- *   251      key weights of a prompt (info0 = sequence, info1 = T_b; a wait)
+ *   251      key weights of a prompt (a sequence's offsets: info0 = sequence, info1 = T_b;
+ *            a wait)
  *   261      eviction's choice (info0 = sequence, info1 = length)
  *   271      eviction's move (info0 = sequence; info1 = a length, a row of
  *            kept, or a block)

@@ -1,11 +1,13 @@
 """A densely attended layer's cache at the ends of what its calls allow:
-values that are infinite, NaN or huge, key weights past the largest number, against the fp64 oracle
-(oracle/dense_cache.py)."""
+values that are infinite, NaN or huge, key weights past the largest number,
+against the fp64 oracle (oracle/dense_cache.py); offsets on the device that
+reach past what the host has named, behind guards."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import dense_cache as C
+import test_gpu_attn_weights as W
 from test_gpu_dense_decode import SHAPES, _check, _f, _paged
 
 pytestmark = pytest.mark.gpu
@@ -102,15 +104,6 @@ def test_values_up_to_the_largest_allowed(M, H, G, d):
 
 # ------------------------------------------------------------------ key weights
 
-def _cu(lens):
-    return [sum(lens[:i]) for i in range(len(lens) + 1)]
-
-
-def _varlen(M, T, S):
-    return M.make_varlen(torch.tensor(_cu(T), dtype=torch.int32).cuda(), torch.tensor(_cu(S), dtype=torch.int32).cuda(),
-                         _cu(T), _cu(S))
-
-
 @pytest.mark.parametrize("H,G,d", SHAPES)
 @pytest.mark.parametrize("T", [40, 700, 3000])
 def test_weights_past_the_largest_number_are_infinite(M, H, G, d, T):
@@ -123,10 +116,64 @@ def test_weights_past_the_largest_number_are_infinite(M, H, G, d, T):
         for t, e in heavy.items():
             x[t] = e
         lse = (-x * np.log(2.0))[:, None].expand(T, H).contiguous()
-        w = M.msa_attn_weights(shape, _varlen(M, [T], [T]), q.cuda(), k.cuda(), lse.cuda(), decay=0.0).cpu()[0]
+        w = M.msa_attn_weights(shape, W._varlen(M, [T], [T]), q.cuda(), k.cuda(), lse.cuda(), decay=0.0).cpu()[0]
         want = (H // G) * torch.flip(torch.cumsum(torch.flip(torch.exp(-lse[:, 0].double()), [0]), 0), [0])
         inf = want > 2.0 ** 128 * 1.01
         assert bool((w[:, inf] == float("inf")).all()) and int(inf.sum()) >= 6
         # beyond `last` sums of ones: exact but for the exponential's 2^-22 (an argument of 0 has no error)
         rest = torch.arange(T) > last
         assert bool(((w[:, rest].double() - want[rest]).abs() <= want[rest] * 2.0 ** -21).all())
+
+
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("cu_q,cu_k,bad", [
+    ([0, 20, 70, 103], [0, 301, 430, 470], {0}),              # a key past the weights' width
+    ([0, 20, 70, 103], [0, 300, 430, 471], {2}),              # past the keys
+    ([0, 20, 70, 104], [0, 300, 430, 470], {2}),              # past the queries
+    ([-1, 20, 70, 103], [0, 300, 430, 470], {0}), ([0, 20, 70, 103], [-1, 299, 430, 470], {0}),
+    ([0, 20, 10, 103], [0, 300, 430, 470], {1, 2}),           # offsets that decrease; then more queries than keys
+    ([0, 20, 70, 103], [0, 300, 200, 470], {1}), ([0, 20, 70, 103], [0, HIGH, 430, 470], {0, 1}),
+    ([0, LOW, 70, 103], [0, 300, 430, 470], {0, 1}), ([0, HIGH, 70, 103], [0, 300, 430, 470], {0, 1}),
+    ([0, 20, 70, HIGH], [0, 300, 430, HIGH], {2}), ([0, 20, 20, 103], [LOW, LOW, HIGH, 470], {0, 2}),
+])
+@pytest.mark.parametrize("captured", [False, True])
+def test_key_weights_keep_to_what_the_host_has_named(M, cu_q, cu_k, bad, captured):
+    # the device's offsets, changed after the description was made: a sequence that reaches past it is reported and left
+    # alone, the others are done by the offsets that they have; guards on both sides of the weights
+    T, S, G, guard = [20, 50, 33], [300, 130, 40], 2, 8192
+    q, k = W._inputs(8, G, 64, T, S, 241)
+    shape = M.make_shape(8, G, 64, 64, 16)
+    lse = W._lse(q, k, T, S, shape.sm_scale) + 3.0
+    seqs = W._varlen(M, T, S)
+    around = torch.full((2 * guard + 3 * G * 300,), 7.0, device="cuda")
+    w = around[guard:-guard].view(3, G, 300)
+    w0 = torch.rand(3, G, 300, generator=torch.Generator().manual_seed(242))
+    ws = torch.empty(M.msa_attn_weights_workspace_size(shape, seqs), dtype=torch.uint8, device="cuda")
+    qd, kd, ld = q.cuda(), k.cuda(), lse.cuda()
+    call = lambda check: M.msa_attn_weights(shape, seqs, qd, kd, ld, weights=w, decay=0.5, ws=ws, check=check)  # noqa: E731
+    if captured:
+        call(True)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(False)
+    w.copy_(w0)
+    seqs._keep[0].copy_(torch.tensor(cu_q, dtype=torch.int32))
+    seqs._keep[1].copy_(torch.tensor(cu_k, dtype=torch.int32))
+    if captured:
+        graph.replay()
+        with pytest.raises(M.MsaError, match="DEVICE_CHECK at site 251"):
+            M._device_check(ws, None, "key weights")
+    else:
+        with pytest.raises(M.MsaError, match="DEVICE_CHECK at site 251"):
+            call(True)
+    got = w.cpu()
+    for b in range(3):
+        if b in bad or cu_q[b + 1] == cu_q[b]:
+            assert torch.equal(got[b], w0[b]), b
+            continue
+        at, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        W._check(got[b:b + 1], q[at], k[keys], lse[at], [cu_q[b + 1] - cu_q[b]], [cu_k[b + 1] - cu_k[b]], shape.sm_scale,
+                 w0[b:b + 1], 0.5)
+    assert bool((around[:guard] == 7.0).all()) and bool((around[-guard:] == 7.0).all())
