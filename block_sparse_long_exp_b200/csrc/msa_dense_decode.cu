@@ -886,7 +886,7 @@ int launch_split(const DenseDecodeArgs& a, int ctas, const CUtensorMap& tm_k, co
   return (int)cudaGetLastError();
 }
 
-int logit_tiles_of(int32_t max_seqlen) { return (max_seqlen + 63) / 64 * 4; }   // whole tiles of every G
+int logit_tiles_of(int32_t max_seqlen) { return (int)(((int64_t)max_seqlen + 63) / 64 * 4); }   // whole tiles of every G
 
 }  // namespace
 
@@ -914,7 +914,7 @@ int launch_dense_decode(const DenseDecodeArgs& a, void* stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return (int)e;
   const int tok = 64 / a.G;
-  const int64_t most = (int64_t)a.batch * ((a.max_seqlen + tok - 1) / tok);     // tiles, at most
+  const int64_t most = (int64_t)a.batch * (((int64_t)a.max_seqlen + tok - 1) / tok);     // tiles, at most
   int ctas = sms < kDecodeCtas ? sms : kDecodeCtas;
   if (most < ctas) ctas = (int)most;
 
@@ -956,7 +956,7 @@ int launch_dense_decode(const DenseDecodeArgs& a, void* stream) {
   }
   if (rc != 0 || !w) return rc;
   ProfScope p("dense_weights", stream);
-  const unsigned gx = (unsigned)((a.max_seqlen + kWeightTiles * kTileTok - 1) / (kWeightTiles * kTileTok));
+  const unsigned gx = (unsigned)(((int64_t)a.max_seqlen + kWeightTiles * kTileTok - 1) / (kWeightTiles * kTileTok));
   for (int b0 = 0; b0 < a.batch; b0 += 65535) {   // grid z is 16 bits
     const int nb = a.batch - b0 < 65535 ? a.batch - b0 : 65535;
     rc = launch_after(dense_weights_kernel, dim3(gx, a.G, nb), 256, st,

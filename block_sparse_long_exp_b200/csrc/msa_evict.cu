@@ -737,7 +737,7 @@ struct LongLayout {
 };
 LongLayout long_layout(int64_t rows, int32_t max_seqlen) {
   LongLayout L{};
-  L.parts = (max_seqlen + kLongPart - 1) / kLongPart;
+  L.parts = (int32_t)(((int64_t)max_seqlen + kLongPart - 1) / kLongPart);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;

@@ -115,6 +115,19 @@ def test_evict_move_host_checks(M):
     assert call(n=300) == WORKSPACE
 
 
+def test_workspaces_of_the_longest_sequence(M):
+    # the longest description that is accepted: round-ups past 2^31
+    lib, shape, most = M.load_library(), M.make_shape(4, 1, 64, 64, 16), 16777213 * 128
+    pg = _pages(M, batch=1, max_blocks=16777213, max_seqlen=most, num_pages=1)
+    keys = -(-most // 4096) * 4096 * 4
+    assert keys <= lib.msa_evict_select_workspace_size(_by(shape), _by(pg), 0) <= keys + 2 ** 24
+    scores = -(-most // 64) * 64 * 4 * 4
+    for with_weights, least in ((0, 0), (1, scores)):
+        assert least <= lib.msa_dense_attn_decode_paged_workspace_size(_by(shape), _by(pg), with_weights) <= least + 2 ** 24
+    pg = _pages(M, batch=1, max_blocks=16777214, max_seqlen=most, num_pages=1)
+    assert lib.msa_evict_select_workspace_size(_by(shape), _by(pg), 0) == 0
+
+
 # ------------------------------------------------------------------ binding
 
 H, G, d, d_idx = 8, 2, 64, 32

@@ -1,7 +1,8 @@
 """A densely attended layer's cache at the ends of what its calls allow:
 values that are infinite, NaN or huge, key weights past the largest number,
 against the fp64 oracle (oracle/dense_cache.py); offsets on the device that
-reach past what the host has named, behind guards."""
+reach past what the host has named, behind guards; the longest sequence that a
+description may name."""
 import numpy as np
 import pytest
 import torch
@@ -177,3 +178,44 @@ def test_key_weights_keep_to_what_the_host_has_named(M, cu_q, cu_k, bad, capture
         W._check(got[b:b + 1], q[at], k[keys], lse[at], [cu_q[b + 1] - cu_q[b]], [cu_k[b + 1] - cu_k[b]], shape.sm_scale,
                  w0[b:b + 1], 0.5)
     assert bool((around[:guard] == 7.0).all()) and bool((around[-guard:] == 7.0).all())
+
+
+# ------------------------------------------------------------------ the longest description
+
+LONGEST = 16777213 * PAGE                                     # 2^31 - 384
+
+
+def test_decode_under_the_longest_description(M):
+    # a short cache whose description names the most that a call takes: 34 GB of scores, 8.6 GB of weights
+    H, G, d, n = 4, 1, 64, 300
+    k, v, table, pages, seqs = _paged([n], G, d, 251, extra_blocks=0)
+    wide = torch.full((1, LONGEST // PAGE), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    q = torch.randn(1, H, d, generator=torch.Generator().manual_seed(252)).bfloat16()
+    shape = M.make_shape(H, G, d, 64, 16)
+    pg = M.make_paged(torch.tensor([n], dtype=torch.int32).cuda(), wide.cuda(), LONGEST, pages)
+    w = torch.empty(1, G, LONGEST, device="cuda")
+    w[:, :, n:n + 100] = 5.0
+    w[:, :, -100:] = 5.0
+    out, lse = M.msa_dense_attn_decode_paged(shape, pg, q.cuda(), k.cuda(), v.cuda(), weights=w, decay=0.0)
+    head = w[:, :, :n].cpu()
+    _check(out.cpu(), lse.cpu(), head, q, seqs, shape.sm_scale, torch.zeros(1, G, n))
+    assert bool((w[:, :, n:n + 100] == 5.0).all()) and bool((w[:, :, -100:] == 5.0).all())
+    del w
+    torch.cuda.empty_cache()
+
+
+def test_choice_under_the_longest_description(M):
+    n, budget = 9000, 700
+    shape = M.make_shape(4, 1, 64, 64, 16)
+    table = torch.zeros(1, LONGEST // PAGE, dtype=torch.int32)
+    pg = M.make_paged(torch.tensor([n], dtype=torch.int32).cuda(), table.cuda(), LONGEST, 1)
+    w = torch.empty(1, 1, LONGEST, device="cuda")
+    head = torch.rand(1, 1, n, generator=torch.Generator().manual_seed(253))
+    w[:, :, :n] = head.cuda()
+    w[:, :, n:n + 5000] = 9.0                                 # past the end: no candidates
+    kept, new = M.msa_evict_select(shape, pg, w, budget, 3, 40)
+    np.testing.assert_array_equal(kept[0].cpu().numpy(), C.evict_select(head[0].numpy(), budget, 3, 40, False))
+    assert new.item() == budget
+    del w
+    torch.cuda.empty_cache()
