@@ -3,7 +3,6 @@
 #include <cuda_runtime.h>
 
 #include <climits>
-#include <cmath>
 
 #include "msa_internal.h"
 #include "msa_cache.h"
@@ -16,8 +15,9 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 bool ws_ok(const void* ws, size_t have, size_t need) { return ws != nullptr && aligned(ws, 256) && have >= need; }
 
-// Keys past a sequence's end count as scores of -inf, which a scale of 0 or below would turn into something else.
-bool scale_ok(float s) { return s > 0.f && std::isfinite(s); }
+// Keys past a sequence's end count as scores of -inf, which the kernels multiply with the scale in units of log2: a scale
+// of 0 or below (a denormal one is 0 there) would turn them into NaN, one past the largest number a score of 0.
+bool scale_ok(float s) { return s >= 0x1p-126f && s * 1.4426950408889634f <= 0x1.fffffep127f; }
 
 bool decay_ok(float d) { return d >= 0.f && d <= 1.f; }
 

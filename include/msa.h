@@ -472,10 +472,11 @@ msa_status_t msa_dense_attn(const msa_shape_t* shape, const msa_varlen_t* seqs,
  * among a sequence's values comes through as the formula has it (in its column of
  * its group alone; as NaN where its weight is below 2^-118 of the largest).  Finite
  * values may be up to 2^88 in size: the sums of larger ones may overflow.
- * q, k_pages, v_pages and out 16-byte aligned, sm_scale positive and finite, else
- * MSA_ERR_INVALID_ARG.  The parts of a sequence are joined in a fixed order: results are the same from
- * run to run (on one device model).  Workspace: with_weights != 0 adds 4 H
- * bytes per sequence and token of max_seqlen (the scores, in 32 bits). */
+ * q, k_pages, v_pages and out 16-byte aligned, sm_scale from 2^-126 to 2.3e38, else
+ * MSA_ERR_INVALID_ARG.  The parts of a sequence are joined in a fixed order:
+ * results are the same from run to run (on one device model).  Workspace:
+ * with_weights != 0 adds 4 H bytes per sequence and token of max_seqlen (the
+ * scores, in 32 bits). */
 size_t msa_dense_attn_decode_paged_workspace_size(const msa_shape_t* shape, const msa_paged_t* pages,
                                                   int32_t with_weights);
 
@@ -500,7 +501,7 @@ msa_status_t msa_dense_attn_decode_paged(const msa_shape_t* shape, const msa_pag
  * are not touched, nor is a sequence without queries.  A (query, head) whose lse
  * is -inf has seen no key and adds nothing.  width >= max_k_len (a paged cache's
  * max_blocks * 128, so that decode steps go on from it), q, k and lse 16-byte
- * aligned, sm_scale positive and finite, else MSA_ERR_INVALID_ARG.  On the device
+ * aligned, sm_scale from 2^-126 to 2.3e38, else MSA_ERR_INVALID_ARG.  On the device
  * a sequence goes by its own two entries of cu_q and cu_k (the first need not be 0):
  * one with more queries than keys, or that reaches past total_q, total_k or the
  * weights' width, is recorded as MSA_ERR_DEVICE_CHECK and left as it is (nothing is

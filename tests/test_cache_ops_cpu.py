@@ -128,6 +128,18 @@ def test_workspaces_of_the_longest_sequence(M):
     assert lib.msa_evict_select_workspace_size(_by(shape), _by(pg), 0) == 0
 
 
+@pytest.mark.parametrize("scale,refused", [(1e-39, True), (1.1e-38, True), (2.0 ** -149, True), (2.4e38, True), (3.4e38, True),
+                                           (2.0 ** -126, False), (2.3e38, False)])
+def test_scales_that_would_break_the_mask_are_refused(M, scale, refused):
+    # denormal scales count as 0 on the device (0 x -inf), 2.4e38 is past the largest number in units of log2
+    lib, shape = M.load_library(), M.make_shape(64, 4, 128, 64, 16, sm_scale=scale)
+    seqs, pg = M.Varlen(1, 64, 300, 0, 64, 300, A, A), _pages(M)
+    # an accepted one is refused for its workspace, which is looked at last
+    want = INVALID if refused else WORKSPACE
+    assert lib.msa_dense_attn_decode_paged(_by(shape), _by(pg), A, A, A, A, None, None, 1.0, A, 256, None) == want
+    assert lib.msa_attn_weights(_by(shape), _by(seqs), A, A, A, A, 300, 1.0, A, 255, None) == want
+
+
 # ------------------------------------------------------------------ binding
 
 H, G, d, d_idx = 8, 2, 64, 32

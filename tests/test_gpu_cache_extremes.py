@@ -103,6 +103,23 @@ def test_values_up_to_the_largest_allowed(M, H, G, d):
     _check(out, lse, None, q, seqs, shape.sm_scale)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -126, 2.3e38])
+def test_scales_at_their_bounds(M, scale):
+    # scores of 0: every key of a sequence weighs the same, whatever stands behind its end
+    H, G, d, lens = 16, 2, 64, [1, 19, 300]
+    k, v, table, pages, seqs = _paged(lens, G, d, 261)
+    shape = M.make_shape(H, G, d, 64, 16, sm_scale=scale)
+    w0 = torch.zeros(3, G, table.shape[1] * PAGE)
+    q = torch.zeros(3, H, d).bfloat16()
+    out, lse, w = _decode(M, shape, lens, table, pages, q, k, v, w0)
+    _check(out, lse, w, q, seqs, scale, w0)
+    kk = torch.cat([a for a, _ in seqs])
+    ones = torch.log(torch.cat([torch.arange(1, n + 1) for n in lens]).float())[:, None].expand(-1, H).contiguous()
+    got = M.msa_attn_weights(shape, W._varlen(M, lens, lens), torch.zeros(sum(lens), H, d).bfloat16().cuda(), kk.cuda(),
+                             ones.cuda()).cpu()
+    W._check(got, torch.zeros(sum(lens), H, d).bfloat16(), kk, ones, lens, lens, scale, torch.zeros(3, G, 300), 1.0)
+
+
 # ------------------------------------------------------------------ key weights
 
 @pytest.mark.parametrize("H,G,d", SHAPES)
