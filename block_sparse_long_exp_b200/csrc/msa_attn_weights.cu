@@ -550,11 +550,11 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 }
 
 // Adds the parts of the key block that begins in run i and ends in another, and
-// makes one error word of the CTAs'.
+// makes one error word of the CTAs'.  (What the kernel ahead writes is read through
+// pointers without __restrict__: const ones with it may be read before the wait.)
 __global__ void __launch_bounds__(kAwKeys)
-weights_join_kernel(const AwOpen* __restrict__ open, const float* __restrict__ part, float* __restrict__ weights,
-                    int64_t width, float decay, int G, const int32_t* __restrict__ cu_k,
-                    const DevError* __restrict__ errors, DevError* __restrict__ err) {
+weights_join_kernel(const AwOpen* open, const float* part, float* __restrict__ weights, int64_t width, float decay, int G,
+                    const int32_t* __restrict__ cu_k, const DevError* errors, DevError* err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0 && threadIdx.x < 32) {      // the first CTA's that found something
     int first = gridDim.x;

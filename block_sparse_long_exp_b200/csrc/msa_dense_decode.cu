@@ -639,14 +639,14 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 // rows of sequences without tokens, and makes one error word of the CTAs'.  WPJ
 // warps have one (b, h) and VEC columns a lane, so that few sequences in many
 // parts and many in few parts both keep the loads in flight: a warp reads the
-// parts w, w + WPJ, ... eight at a time.
+// parts w, w + WPJ, ... eight at a time.  (What the kernel ahead writes is read through
+// pointers without __restrict__: const ones with it may be read before the wait.)
 constexpr int kMaxParts = (kDecodeCtas + 31) / 32 * 32;
 template <int D, int WPJ, int VEC>
 __global__ void __launch_bounds__(256)
 dense_join_kernel(__nv_bfloat16* __restrict__ out, float* __restrict__ lse, int batch, int H, int G,
-                  const int32_t* __restrict__ seqlens, int max_seqlen, const float2* __restrict__ part_ml,
-                  const float* __restrict__ part_o, float2* __restrict__ stats, int ctas,
-                  const DevError* __restrict__ errors, DevError* __restrict__ err) {
+                  const int32_t* __restrict__ seqlens, int max_seqlen, const float2* part_ml, const float* part_o,
+                  float2* __restrict__ stats, int ctas, const DevError* errors, DevError* err) {
   constexpr int JPC = 8 / WPJ;                   // (b, h) pairs per CTA
   constexpr int CB = D / (32 * VEC);             // CTAs that share a pair's columns
   constexpr int BATCH = 8;                       // parts in flight per warp
@@ -814,7 +814,7 @@ dense_join_kernel(__nv_bfloat16* __restrict__ out, float* __restrict__ lse, int 
 // token and group).
 constexpr int kWeightTiles = 32;                 // 16-token tiles per CTA
 __global__ void __launch_bounds__(256)
-dense_weights_kernel(const float* __restrict__ logits, const float2* __restrict__ stats, float* __restrict__ weights,
+dense_weights_kernel(const float* logits, const float2* stats, float* __restrict__ weights,
                      int H, int G, float c, float decay, const int32_t* __restrict__ seqlens, int max_seqlen,
                      int64_t width, int logit_tiles) {
   const int b = blockIdx.z, g = blockIdx.y, Hg = H / G;

@@ -2,6 +2,9 @@
 and the Python binding refuse before any launch, workspace sizes, and the fp64
 oracle (oracle/dense_cache.py) pinned by small cases worked out here."""
 import ctypes
+import glob
+import os
+import re
 
 import numpy as np
 import pytest
@@ -138,6 +141,22 @@ def test_scales_that_would_break_the_mask_are_refused(M, scale, refused):
     want = INVALID if refused else WORKSPACE
     assert lib.msa_dense_attn_decode_paged(_by(shape), _by(pg), A, A, A, A, None, None, 1.0, A, 256, None) == want
     assert lib.msa_attn_weights(_by(shape), _by(seqs), A, A, A, A, 300, 1.0, A, 255, None) == want
+
+
+def test_chained_kernels_read_what_the_one_ahead_writes_after_the_wait(M):
+    # a kernel that starts before the one ahead of it has ended: `const T* __restrict__` tells the compiler that nothing
+    # changes the data while it runs, so that its loads may move ahead of the wait; only a call's inputs may have it
+    inputs, seen = {"seqlens", "cu_k"}, 0
+    for path in glob.glob(os.path.join(os.path.dirname(M.__file__), "csrc", "*.cu")):
+        for kernel in open(path, encoding="utf-8").read().split("__global__")[1:]:
+            head, body = kernel.split("{", 1)
+            body = body.split("\n}\n", 1)[0]
+            if "pdl_wait()" not in body and "griddepcontrol.wait" not in body:
+                continue
+            seen += 1
+            held = set(re.findall(r"const\s+\w+\s*\*\s*__restrict__\s+(\w+)", head))
+            assert held <= inputs, (os.path.basename(path), head.strip()[:60], held - inputs)
+    assert seen >= 8
 
 
 # ------------------------------------------------------------------ binding
