@@ -133,8 +133,12 @@ msa_status_t msa_evict_move(const msa_shape_t* shape, const msa_paged_t* pages, 
   if (new_pages->batch != pages->batch || new_pages->num_pages != pages->num_pages) return MSA_ERR_INVALID_ARG;
   if (!kept || kept_width < 1 || !k_pages || !v_pages) return MSA_ERR_INVALID_ARG;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_idx_pages, 16)) return MSA_ERR_INVALID_ARG;
-  if ((weights == nullptr) != (weights_out == nullptr) || (weights != nullptr && weights == weights_out))
-    return MSA_ERR_INVALID_ARG;
+  if ((weights == nullptr) != (weights_out == nullptr)) return MSA_ERR_INVALID_ARG;
+  if (weights != nullptr) {                       // rows go out while others are still read
+    const uintptr_t row = (uintptr_t)pages->batch * shape->G * kBk * sizeof(float);
+    const uintptr_t in = reinterpret_cast<uintptr_t>(weights), to = reinterpret_cast<uintptr_t>(weights_out);
+    if (in < to + row * new_pages->max_blocks && to < in + row * pages->max_blocks) return MSA_ERR_INVALID_ARG;
+  }
   // the groups share the index keys: tokens kept by group have none of their own
   if (per_group != 0 && shape->G > 1 && k_idx_pages != nullptr) return MSA_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, msa_evict_move_workspace_size(shape, pages))) return MSA_ERR_WORKSPACE;

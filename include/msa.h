@@ -559,7 +559,7 @@ msa_status_t msa_evict_select(const msa_shape_t* shape, const msa_paged_t* pages
  *   weights, weights_out  both or neither: [batch, G, max_blocks*128] of
  *                         `pages`, and of new_pages (out): the kept tokens'
  *                         weights, zeros from the new length on.  They must
- *                         not overlap.
+ *                         not overlap (else MSA_ERR_INVALID_ARG).
  * kept as from msa_evict_select, kept_width its last dimension.  Keys carry
  * their rotary position in them, so rows are copied as they are.  Rows of the
  * last new page past the new length are not touched.  Recorded as

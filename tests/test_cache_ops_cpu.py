@@ -159,6 +159,17 @@ def test_chained_kernels_read_what_the_one_ahead_writes_after_the_wait(M):
     assert seen >= 8
 
 
+def test_the_move_refuses_weights_that_overlap(M):
+    # 2 x 4 x 8 pages of weights in, 2 x 4 x 2 out: 32768 and 8192 bytes
+    lib, shape, pg, new = M.load_library(), M.make_shape(64, 4, 128, 64, 16), _pages(M), _pages(M, max_blocks=2, max_seqlen=200)
+    base = 1 << 20
+    for out, refused in ((base, True), (base + 4, True), (base + 32764, True), (base + 32768, False), (base - 8188, True),
+                         (base - 8192, False), (base + 16384, True)):
+        # an accepted pair is refused for its workspace, which is looked at last
+        assert lib.msa_evict_move(_by(shape), _by(pg), _by(new), A, 200, 0, A, A, None, base, out, A, 300, None) == \
+            (INVALID if refused else WORKSPACE), out
+
+
 # ------------------------------------------------------------------ binding
 
 H, G, d, d_idx = 8, 2, 64, 32
