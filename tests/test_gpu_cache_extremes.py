@@ -2,13 +2,16 @@
 values that are infinite, NaN or huge, key weights past the largest number,
 against the fp64 oracle (oracle/dense_cache.py); offsets on the device that
 reach past what the host has named, behind guards; the longest sequence that a
-description may name."""
+description may name; and the choice by the groups' sum among weights whose sums are
+denormal, past the largest number, NaN or next to nothing, in every launch form,
+exactly."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import dense_cache as C
 import test_gpu_attn_weights as W
+import test_gpu_evict as E
 from test_gpu_dense_decode import SHAPES, _check, _f, _paged
 
 pytestmark = pytest.mark.gpu
@@ -236,3 +239,57 @@ def test_choice_under_the_longest_description(M):
     assert new.item() == budget
     del w
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ sums of the groups' weights
+
+def _group_weights(B, G, blocks, kind, seed):
+    g = torch.Generator().manual_seed(seed)
+    shape = (B, G, blocks * PAGE)
+    if kind in ("odd", "denormal"):
+        return E._weights(B, G, blocks, seed, kind)
+    if kind == "huge":                                        # sums past the largest number, of both signs, and just below it
+        w = 3.4e38 * (0.02 + 0.98 * torch.rand(shape, generator=g))
+        return torch.where(torch.rand(shape, generator=g) < 0.3, -w, w)
+    if kind == "edge":                                        # sums that round to the largest number or to infinity, by a bit
+        top = np.array(0x7f7fffff, np.int32).view(np.float32)
+        w = torch.randint(0, 4, shape, generator=g).float() * 2.0 ** 103      # halves of the last place of the largest
+        w[:, 0] = torch.where(torch.rand(shape[0], shape[2], generator=g) < 0.8, torch.tensor(top), w[:, 0])
+        return w
+    if kind == "halves":                                      # sums half way between two numbers: to the even one
+        w = torch.randint(0, 5, shape, generator=g).float() * 0.5
+        w[:, 0] = torch.randint(2 ** 24 - 3, 2 ** 24 + 3, (shape[0], shape[2]), generator=g).float()
+        w[:, 0] *= torch.where(torch.rand(shape[0], shape[2], generator=g) < 0.2, -1.0, 1.0)
+        return w
+    assert kind == "cancel"                                   # sums far below their terms, denormal ones and zeros among them
+    w = torch.exp2(torch.randint(-149, 128, shape, generator=g).double()).float() * (1 + torch.rand(shape, generator=g)).clamp(max=1.99)
+    w[:, 1] = -w[:, 0] * (1 + 2.0 ** -23 * torch.randint(-2, 3, (shape[0], shape[2]), generator=g).float())
+    if G > 2:
+        w[:, 2:] *= (torch.rand(B, 1, shape[2], generator=g) < 0.3)
+    return w
+
+
+@pytest.mark.parametrize("G", [2, 4])
+@pytest.mark.parametrize("kind", ["odd", "denormal", "huge", "edge", "halves", "cancel"])
+@pytest.mark.parametrize("L,B", [(1000, 1), (4096, 2), (8000, 1), (20000, 1), (66000, 1), (9000, 49)])
+def test_choice_by_the_sum_of_odd_weights(M, G, kind, L, B):
+    # four or eight tokens a thread, a cluster, a CTA per part (long, and many rankings)
+    lens = [L - 37 * b for b in range(B)]
+    w = _group_weights(B, G, -(-L // PAGE), kind, 271 + G)
+    with np.errstate(over="ignore", invalid="ignore"):
+        score = w.double().sum(1).float()
+    # budgets that end among infinities, in the middle, among NaN or the smallest ones
+    for budget, sink, recent in ((L // 10, 0, 0), (L // 2, 5, 33), (L - L // 20, 0, 7)) if B == 1 else ((L // 3, 3, 9),):
+        if B <= 2:
+            E._select(M, w, lens, budget, sink, recent, False)
+            continue
+        kept, new = M.msa_evict_select(M.make_shape(4 * G, G, 64, 64, 16), E._pages(M, lens, blocks=w.shape[2] // PAGE),
+                                       w.cuda(), budget, sink, recent)
+        assert new.cpu().tolist() == [min(n, budget) for n in lens]
+        for b, n in enumerate(lens):
+            s = score[b, :n].numpy()
+            # descending, NaN last, ties (zeros of both signs among them) to the lower position
+            order = np.lexsort((np.arange(n), np.where(np.isnan(s), 0.0, -s.astype(np.float64)), np.isnan(s)))
+            middle = order[(order >= sink) & (order < n - recent)][:budget - sink - recent]
+            want = np.sort(np.concatenate([np.arange(sink), middle, np.arange(n - recent, n)]))
+            np.testing.assert_array_equal(kept[b, 0].cpu().numpy()[:min(n, budget)], want if n > budget else np.arange(n))
