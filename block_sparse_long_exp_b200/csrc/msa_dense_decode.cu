@@ -625,8 +625,8 @@ dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           if ((lane & 3) == 0) part_ml[at] = make_float2(m[y], l[y]);
         }
       }
-      if (odd) {                                  // (a row without any weight keeps its zeros)
-        const uint32_t rows = (r < Hg && !(whole && l[0] == 0.f) ? 1u : 0u) | (r + 8 < Hg && !(whole && l[1] == 0.f) ? 2u : 0u);
+      if (odd) {                                  // (a row without any weight keeps its zeros, one with a NaN among them its NaN)
+        const uint32_t rows = (r < Hg && (!whole || l[0] > 0.f) ? 1u : 0u) | (r + 8 < Hg && (!whole || l[1] > 0.f) ? 2u : 0u);
         put_infinities<D>(v_pages, G, g, block_table + (int64_t)b * max_blocks, num_pages, L, t0 - s, e - s,
                           whole ? out + ((int64_t)b * H + g * Hg) * D : nullptr,
                           part_o + (((int64_t)blockIdx.x * 2 + slot) * H + g * Hg) * D, rows);

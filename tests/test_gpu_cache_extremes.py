@@ -90,6 +90,26 @@ def test_values_of_heads_that_see_nothing_do_not_count(M, H, G, d):
         assert torch.all(torch.isfinite(out[0, H // G:].float())) and torch.all(torch.isfinite(lse[0, H // G:]))
 
 
+@pytest.mark.parametrize("H,G,d", [(8, 2, 64), (32, 2, 128)])
+@pytest.mark.parametrize("n", [3, 17, 300, 9000])
+def test_a_score_of_nan_leaves_nothing_but_nan(M, H, G, d, n):
+    # a NaN or infinity among the keys of group 0, infinities among its values: every weight of the group is NaN
+    for x in (float("nan"), float("inf")):
+        k, v, table, pages, seqs = _paged([n, 5], G, d, 226)
+        at = _rows(table, 0, n)
+        k[at[n // 2], 0, 0] = x
+        v[at, 0, 1], v[at[0], 0, 5] = float("inf"), float("-inf")
+        q = (torch.rand(2, H, d, generator=torch.Generator().manual_seed(227)) + 0.5).bfloat16()
+        shape = M.make_shape(H, G, d, 64, 16)
+        w0 = torch.rand(2, G, table.shape[1] * PAGE)
+        out, lse, w = _decode(M, shape, [n, 5], table, pages, q, k, v, w0)
+        hg = H // G
+        assert torch.all(torch.isnan(out[0, :hg].float())) and torch.all(torch.isnan(lse[0, :hg]))
+        assert torch.all(torch.isnan(w[0, 0, :n])) and torch.equal(w[0, 0, n:], w0[0, 0, n:])
+        _check(out[:, hg:2 * hg], lse[:, hg:2 * hg], w[:, 1:2], q[:, hg:2 * hg],
+               [(a[:, 1:2].contiguous(), b[:, 1:2].contiguous()) for a, b in seqs], shape.sm_scale, w0[:, 1:2])
+
+
 @pytest.mark.parametrize("H,G,d", [(8, 2, 64), (64, 4, 128), (16, 1, 64)])
 def test_values_up_to_the_largest_allowed(M, H, G, d):
     # sizes from 2^80 to 2^88, of both signs
