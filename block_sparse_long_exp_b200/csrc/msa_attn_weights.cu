@@ -93,10 +93,10 @@ __device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {   // N
   return r;
 }
 // acc += 2^x without the exponential's unit, by Cody and Waite's reduction: x =
-// i + f with i whole and |f| <= 1/2, 2^f a polynomial of degree 5 (fitted to the smallest largest relative
-// error over [-1/2, 1/2]: 2^-23.7, with the roundings 2^-22.2; the unit's own
-// is 2^-22), and 2^i a number whose exponent field is i + 127: what x + 3 2^22 +
-// 127 has in its low bits.  Below -127 the result is 0, from 127.5 on infinite.
+// i + f with i whole and |f| <= 1/2, 2^f a polynomial of degree 5 (its relative
+// error is below 2^-22.5 over [-1/2, 1/2], below 2^-22 with the roundings; the unit's
+// own is 2^-22), and 2^i a number whose exponent field is i + 127: what x +
+// 3 2^22 + 127 has in its low bits.  Below -127 the result is 0, from 127.5 on infinite.
 __device__ __forceinline__ uint64_t add_exp2_poly(uint64_t x, uint64_t acc) {
   float a, b;
   unpair(x, a, b);

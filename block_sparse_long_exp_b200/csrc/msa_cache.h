@@ -77,7 +77,7 @@ struct DenseDecodeArgs {
   DevError* err;              // written by the join
   // workspace slices (dense_decode_layout)
   DevError* errors;           // [CTA]
-  float2* stats;              // [batch, H]: maximum and sum of each head's softmax
+  float2* stats;              // [batch, H]: m (the largest score in units of log2, or up to 8 below it) and sum of 2^(score - m)
   float2* part_ml;            // [CTA, 2, H]
   float* part_o;              // [CTA, 2, H, d]
   float* logits;              // scores of every key (with weights only)

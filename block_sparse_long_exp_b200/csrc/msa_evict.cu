@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kLongThreads) long_write_kernel(const LongArgs
   const int tid = threadIdx.x;
   pdl_wait();
   if (!p.cut || p.n == 0) return;
-  uint4 k[kLongPer / 4];                          // 16 tokens in a row
+  uint4 k[kLongPer / 4];                          // 8 tokens in a row
   const uint4* keys = reinterpret_cast<const uint4*>(a.keys + (int64_t)blockIdx.x * kLongPart + tid * kLongPer);
 #pragma unroll
   for (int s = 0; s < kLongPer / 4; ++s) k[s] = keys[s];

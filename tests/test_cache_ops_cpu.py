@@ -170,6 +170,26 @@ def test_the_move_refuses_weights_that_overlap(M):
             (INVALID if refused else WORKSPACE), out
 
 
+def test_error_of_the_polynomial_exponential(M):
+    # the coefficients as they stand in the source: their error in 64 bits, and with the kernel's 32-bit steps (a fused
+    # multiply-add rounds once), over [-1/2, 1/2] as its comment gives them
+    src = open(os.path.join(os.path.dirname(M.__file__), "csrc", "msa_attn_weights.cu"), encoding="utf-8").read()
+    body = src[src.index("uint64_t add_exp2_poly"):]
+    body = body[:body.index("\n}\n")]
+    found = re.findall(r"uint64_t p = pair\(([\d.]+)f|p = fma2\(p, f, pair\(([\d.]+)f", body)
+    c = [np.float32(a or b) for a, b in found]
+    assert len(c) == 6 and c[-1] == 1.0
+    f = np.linspace(-0.5, 0.5, 400001).astype(np.float32)
+    exact, p, q = np.exp2(f.astype(np.float64)), np.zeros(f.shape), np.full(f.shape, c[0], np.float32)
+    for x in c:
+        p = p * f + float(x)
+    for x in c[1:]:
+        q = (q.astype(np.float64) * f + float(x)).astype(np.float32)
+    pure, rounded = (float(np.log2(np.abs(y / exact - 1).max())) for y in (p, q))
+    assert pure < -22.5 and "below 2^-22.5 over" in src
+    assert rounded < -22.0 and "below 2^-22 with the roundings" in src
+
+
 # ------------------------------------------------------------------ binding
 
 H, G, d, d_idx = 8, 2, 64, 32
