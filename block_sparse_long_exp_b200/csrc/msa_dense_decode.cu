@@ -11,9 +11,9 @@
 //
 // The step is bound by HBM: every cached key and value is read once and meets
 // H / G query heads, 16 operations a byte at most.  On a B200 (H 64, G 4, d 128):
-// 32 caches of 1..8192 tokens 55.7 us (283 MB; 43 at the rate of a copy), one of
-// 1M 331 us on a cool device (6.5 TB/s) and 372 in a row, at the board's power
-// limit; the loads alone take 306.
+// 32 caches of 1..8192 tokens 53 to 54 us (283 MB; 43 at the rate of a copy), one of
+// 1M 308 to 320 us in a row (6.7 to 7.0 TB/s); the loads alone take 306.  At H 32, G 4,
+// d 64, 32 caches of 8192 tokens take 48 us (41 at the rate of a copy).
 //   split : the caches are cut into tiles of 64 / G tokens with all G groups
 //           (16 KB of keys and as much of values at d = 128, contiguous in the
 //           page), and the tiles of all sequences, in order, into equal runs,
@@ -32,8 +32,10 @@
 //   weights: the scores are kept in 32 bits (a 16-bit score would be off by
 //           2^-9 of its size, so its weight by per cents) and read again once m
 //           and l are known: 8 H bytes a token next to the 4 G d of K and V.
-//           Reading K again would cost 2 G d.  2 x 262K..400K tokens: 305 us,
-//           16 x 1K..16K (H 32, G 2) 53.6.
+//           Reading K again would cost 2 G d.  2 x 262K..400K tokens: 301 to
+//           308 us, 16 x 1K..16K (H 32, G 2) 54.  The pass has a CTA per 512 tokens
+//           of max_seqlen and leaves where a sequence has ended: 16 x 2K tokens take 31
+//           us under a max_seqlen of 2K and 39 under one of 128K.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -207,8 +209,9 @@ __device__ __noinline__ void put_infinities(const __nv_bfloat16* __restrict__ v_
 }
 
 // kFew: at most eight heads a group.  The rows that they leave of the second
-// product's operand then hold the remainders: one product does for both terms (8 x
-// 64K tokens, H 32, G 4, d 128: 171 us; 178 with two).
+// product's operand then hold the remainders: one product does for both terms (in a
+// graph, H 32, G 4: 8 x 64K tokens at d 64 83.6 us, 87.8 with two; at d 128 156.5 and
+// 157.2).
 template <int D, bool kWeights, bool kFew>
 __global__ void __launch_bounds__(kDecThreads, 1)
 dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -942,7 +945,9 @@ int launch_dense_decode(const DenseDecodeArgs& a, void* stream) {
   {
     ProfScope p("dense_join", stream);
     // few sequences lie in many runs each: eight warps to a (b, h), and up to two sequences its columns over 2 or 4
-    // CTAs; many lie in few: one warp
+    // CTAs; many lie in few: one warp.  The three forms, in a graph, H 64, G 4, d 128 (a whole call): 2 x 130K tokens
+    // 85.6, 85.7 and 93.5 us, 3 x 87K 87.0, 84.2, 90.6, 16 x 16K 103, 88.2, 86.1, 32 x 8K 123, 94.2, 84.6; d 64, H 32:
+    // 16 x 16K 48.2, 45.8, 46.9, 32 x 8K 53.0, 48.4, 46.3
 #define MSA_JOIN(DD, W, VEC)                                                                                       \
   rc = launch_after(dense_join_kernel<DD, W, VEC>,                                                                 \
                     dim3((unsigned)((pairs + 8 / W - 1) / (8 / W) * (DD / (32 * VEC)))), 256, st, out, a.lse, a.batch,     \
