@@ -242,8 +242,8 @@ template <int D>
 __global__ void __launch_bounds__(kAwThreads, 1)
 attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                     const float* __restrict__ lse, float* __restrict__ weights, int64_t width, float decay, int batch,
-                    int H, int G, int qt_log, float scale_log2, const Seqs seqs, AwOpen* __restrict__ open, float* __restrict__ part,
-                    DevError* errors) {
+                    int H, int G, int qt_log, float scale_log2, const Seqs seqs, AwOpen* __restrict__ open,
+                    float* __restrict__ part, DevError* errors) {
   constexpr int NQ = num_q<D>();
   constexpr int KST = k_stage<D>(), QST = q_stage<D>();
   // the swizzled tiles want 1024-byte boundaries; there is no room to round up (this kernel has no other shared memory)
@@ -299,7 +299,8 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       fence_mbar_init();
     }
     __syncthreads();
-    if (blockIdx.x == 0 && bad >= 0) report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, bad, seqs.cu_q[bad + 1] - seqs.cu_q[bad]);
+    if (blockIdx.x == 0 && bad >= 0)
+      report_error(err, MSA_ERR_DEVICE_CHECK, kSiteAttnWeights, bad, seqs.cu_q[bad + 1] - seqs.cu_q[bad]);
     int64_t before = 0, total = 0;
     for (int w = 0; w < kAwThreads / 32; ++w) {
       if (w < warp) before += ctl->warp_sum[w];
@@ -598,7 +599,8 @@ int launch_units(const AttnWeightsArgs& a, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
   const int rc = allow_smem(attn_weights_kernel<D>, smem, &ready);
   if (rc != 0) return rc;
-  const Seqs seqs{a.cu_q, a.cu_k, (int32_t)a.total_q, (int32_t)a.total_k, (int32_t)(a.width < INT32_MAX ? a.width : INT32_MAX)};
+  const Seqs seqs{a.cu_q, a.cu_k, (int32_t)a.total_q, (int32_t)a.total_k,
+                  (int32_t)(a.width < INT32_MAX ? a.width : INT32_MAX)};
   ProfScope p("attn_weights", st);
   attn_weights_kernel<D><<<ctas, kAwThreads, smem, st>>>(
       tm_k, tm_q, a.lse, a.weights, a.width, a.decay, a.batch, a.H, a.G, qt_log, a.sm_scale * kLog2e, seqs,

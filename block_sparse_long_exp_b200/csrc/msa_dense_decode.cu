@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 dense_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ v_pages,
                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int batch, int H, int G, float sm_scale,
-                    const int32_t* __restrict__ seqlens,
-                    const int32_t* __restrict__ block_table, int max_blocks, int max_seqlen, int64_t num_pages,
+                    const int32_t* __restrict__ seqlens, const int32_t* __restrict__ block_table, int max_blocks,
+                    int max_seqlen, int64_t num_pages,
                     float2* __restrict__ stats, float2* __restrict__ part_ml, float* __restrict__ part_o,
                     float* __restrict__ logits, int logit_tiles, DevError* errors) {
   constexpr int NST = num_stages<D>();

@@ -470,8 +470,9 @@ msa_status_t msa_dense_attn(const msa_shape_t* shape, const msa_varlen_t* seqs,
  * page past the sequence's end may hold anything.  A head whose scores are all
  * -inf gets out 0 and lse -inf, whatever the values are.  An infinity or NaN
  * among a sequence's values comes through as the formula has it (in its column of
- * its group alone; as NaN where its weight is below 2^-118 of the largest).  Finite
- * values may be up to 2^88 in size: the sums of larger ones may overflow.
+ * its group alone; where its weight is below 2^-118 of the largest, 0 included, an
+ * infinity comes as itself or as NaN).  Finite values may be up to 2^88 in size: the
+ * sums of larger ones may overflow.
  * q, k_pages, v_pages and out 16-byte aligned, sm_scale from 2^-126 to 2.3e38, else
  * MSA_ERR_INVALID_ARG.  The parts of a sequence are joined in a fixed order:
  * results are the same from run to run (on one device model).  Workspace:
